@@ -5,14 +5,18 @@ The functions named like the C entry points (``nvfp4_quantize``,
 ``nvfp4_quantize_2d``, ``nvfp4_quantize_cast_transpose``, ``nvfp4_rht``,
 ``nvfp4_dequantize``, ``nvfp4_gemm``, ``nvfp4_gemm_ex``,
 ``nvfp4_quantize_with_amax``, and ``mxfp4_quantize``,
-``mxfp4_dequantize``, ``mxfp4_gemm``) only marshal torch
+``mxfp4_dequantize``, ``mxfp4_gemm``, ``nvfp4_gated_ffn``,
+``nvfp4_gated_ffn_grad``, ``nvfp4_quantize_cast_transpose_with_amax``,
+``nvfp4_distill_topk``, ``nvfp4_embed``, ``nvfp4_embed_grad``) only marshal torch
 tensors into pointers and the current HIP stream; every step of the
 computation runs in the library's HIP kernels.  There is no CPU fallback: if
 the library is missing, or a tensor is not on the GPU, the call raises.
 
 Convenience wrappers (``quantize``, ``quantize_2d``,
 ``quantize_cast_transpose``, ``rht``, ``dequantize``, ``gemm``, ``mx_quantize``,
-``mx_dequantize``, ``mx_gemm``)
+``mx_dequantize``, ``mx_gemm``, ``gated_ffn``, ``gated_ffn_grad``,
+``gated_ffn_backward``, ``distill_topk``, ``distill_topk_loss_and_grad``,
+``distill_topk_grad``, ``embed``, ``embed_grad``)
 allocate the outputs with torch (device memory only) and call the same
 entry points.
 """
@@ -28,6 +32,7 @@ LIB_PATH = os.path.join(_HERE, "libnvfp4.so")
 
 F32, BF16 = 0, 1
 RNE, SR = 0, 1
+SILU, GELU = 0, 1
 STATUS = {0: "ok", -1: "invalid argument", -2: "invalid shape", -3: "misaligned pointer",
           -4: "HIP error"}
 
@@ -75,6 +80,19 @@ def lib():
         L.mxfp4_dequantize.argtypes = [P, P, I64, I64, I, P, P]
         L.mxfp4_gemm.restype = I
         L.mxfp4_gemm.argtypes = [P, P, P, P, I64, I64, I64, P, P]
+        F = ctypes.c_float
+        L.nvfp4_quantize_cast_transpose_with_amax.restype = I
+        L.nvfp4_quantize_cast_transpose_with_amax.argtypes = [P, I, I64, I64, I, U64, U64, P, P, P, P, P, P, P]
+        L.nvfp4_gated_ffn.restype = I
+        L.nvfp4_gated_ffn.argtypes = [P, P, P, P, P, P, I64, I64, I64, I, P, I, P]
+        L.nvfp4_gated_ffn_grad.restype = I
+        L.nvfp4_gated_ffn_grad.argtypes = [P, P, P, P, P, P, I64, I64, I64, I, P, P, I, P, P]
+        L.nvfp4_distill_topk.restype = I
+        L.nvfp4_distill_topk.argtypes = [P, I, I64, I64, I64, P, P, I64, P, F, P, P, P, P]
+        L.nvfp4_embed.restype = I
+        L.nvfp4_embed.argtypes = [P, I64, P, I, I64, I64, F, P, P]
+        L.nvfp4_embed_grad.restype = I
+        L.nvfp4_embed_grad.argtypes = [P, I64, P, I, I64, I64, F, P, P]
         L.nvfp4_status_string.restype = ctypes.c_char_p
         L.nvfp4_status_string.argtypes = [I]
         L.nvfp4_last_error.restype = ctypes.c_char_p
@@ -262,6 +280,104 @@ def mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, M, N, K, c):
                             int(K), _ptr(c), _stream(c)), "mxfp4_gemm")
 
 
+def nvfp4_quantize_cast_transpose_with_amax(x, rounding, seed, seed_t, codes, scales, tensor_scale, codes_t,
+                                            scales_t, tensor_scale_t):
+    rows, cols, dev = _want_input(x)
+    _want_quantized(rows, cols, dev, codes, scales, tensor_scale, codes_t, scales_t,
+                    transposed_optional=False)
+    _want(tensor_scale_t, "tensor_scale_t", _F32, dev, min_numel=2)
+    _check(lib().nvfp4_quantize_cast_transpose_with_amax(
+        _ptr(x), _dtype(x), rows, cols, int(rounding), int(seed), int(seed_t), _ptr(codes), _ptr(scales),
+        _ptr(tensor_scale), _ptr(codes_t), _ptr(scales_t), _ptr(tensor_scale_t), _stream(x)),
+        "nvfp4_quantize_cast_transpose_with_amax")
+
+
+def _want_ffn(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, device):
+    _want(x_codes, "x_codes", _U8, device, (M, K // 2))
+    _want(x_scales, "x_scales", _U8, device, (M, K // 16))
+    _want(w_codes, "w_codes", _U8, device, (2 * F, K // 2))
+    _want(w_scales, "w_scales", _U8, device, (2 * F, K // 16))
+    _want(x_tensor_scale, "x_tensor_scale", _F32, device, min_numel=1)
+    _want(w_tensor_scale, "w_tensor_scale", _F32, device, min_numel=1)
+
+
+def nvfp4_gated_ffn(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, act, h):
+    _want(h, "h", _IN, h.device if isinstance(h, torch.Tensor) else None, (M, F))
+    _want_ffn(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, h.device)
+    _check(lib().nvfp4_gated_ffn(_ptr(x_codes), _ptr(x_scales), _ptr(x_tensor_scale), _ptr(w_codes),
+                                 _ptr(w_scales), _ptr(w_tensor_scale), int(M), int(F), int(K), int(act), _ptr(h),
+                                 _dtype(h), _stream(h)), "nvfp4_gated_ffn")
+
+
+def nvfp4_gated_ffn_grad(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, act, dh,
+                         dgu, dgu_amax=None):
+    _want(dgu, "dgu", _IN, dgu.device if isinstance(dgu, torch.Tensor) else None, (M, 2 * F))
+    _want(dh, "dh", (dgu.dtype,), dgu.device, (M, F))
+    _want_ffn(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, dgu.device)
+    _want(dgu_amax, "dgu_amax", _F32, dgu.device, min_numel=1, optional=True)
+    _check(lib().nvfp4_gated_ffn_grad(_ptr(x_codes), _ptr(x_scales), _ptr(x_tensor_scale), _ptr(w_codes),
+                                      _ptr(w_scales), _ptr(w_tensor_scale), int(M), int(F), int(K), int(act),
+                                      _ptr(dh), _ptr(dgu), _dtype(dgu), _ptr(dgu_amax), _stream(dgu)),
+           "nvfp4_gated_ffn_grad")
+
+
+_I32 = (torch.int32,)
+
+
+def nvfp4_distill_topk(logits, idx, top, weight, temperature, loss, lse, grad):
+    """Rows of logits may lie further apart than they are long (a slice of a
+    padded vocabulary); every other tensor is contiguous."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("nvfp4: logits must be a 2-D tensor")
+    T, V = logits.shape
+    dev = logits.device
+    if logits.dtype not in _IN:
+        raise ValueError(f"nvfp4: logits must be torch.float32 or torch.bfloat16, got {logits.dtype}")
+    stride = logits.stride(0) if T > 1 else V
+    if (V > 1 and logits.stride(1) != 1) or stride < V:
+        raise ValueError("nvfp4: logits must have contiguous rows")
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 2:
+        raise ValueError("nvfp4: idx must be a 2-D tensor")
+    K = idx.shape[1]
+    _want(idx, "idx", _I32, dev, (T, K))
+    _want(top, "top", _F32, dev, (T, K))
+    _want(weight, "weight", _F32, dev, (T,), optional=True)
+    _want(loss, "loss", _F32, dev, (T,), optional=True)
+    _want(lse, "lse", _F32, dev, (T,))
+    _want(grad, "grad", (logits.dtype,), dev, (T, V), optional=True)
+    if not logits.is_cuda:
+        raise ValueError("nvfp4: tensors must live in GPU memory (no CPU path)")
+    _check(lib().nvfp4_distill_topk(ctypes.c_void_p(logits.data_ptr()), _dtype(logits), T, V, stride, _ptr(idx),
+                                    _ptr(top), K, _ptr(weight), float(temperature), _ptr(loss), _ptr(lse),
+                                    _ptr(grad), _stream(logits)), "nvfp4_distill_topk")
+
+
+def _want_tokens(tokens, device):
+    if not isinstance(tokens, torch.Tensor) or tokens.dim() != 1:
+        raise ValueError("nvfp4: tokens must be a 1-D tensor")
+    _want(tokens, "tokens", _I32, device)
+    return tokens.shape[0]
+
+
+def nvfp4_embed(tokens, table, scale, out):
+    V, D, dev = _want_input(table, "table")
+    T = _want_tokens(tokens, dev)
+    _want(out, "out", (table.dtype,), dev, (T, D))
+    _check(lib().nvfp4_embed(_ptr(tokens), T, _ptr(table), _dtype(table), V, D, float(scale), _ptr(out),
+                             _stream(table)), "nvfp4_embed")
+
+
+def nvfp4_embed_grad(tokens, dout, scale, grad):
+    T, D, dev = _want_input(dout, "dout")
+    if _want_tokens(tokens, dev) != T:
+        raise ValueError(f"nvfp4: tokens must have {T} elements, got {tokens.shape[0]}")
+    if not isinstance(grad, torch.Tensor) or grad.dim() != 2:
+        raise ValueError("nvfp4: grad must be a 2-D tensor")
+    _want(grad, "grad", _F32, dev, (grad.shape[0], D))
+    _check(lib().nvfp4_embed_grad(_ptr(tokens), T, _ptr(dout), _dtype(dout), grad.shape[0], D, float(scale),
+                                  _ptr(grad), _stream(dout)), "nvfp4_embed_grad")
+
+
 # ---- convenience wrappers ---------------------------------------------------
 @dataclass
 class Quantized:
@@ -391,3 +507,102 @@ def gemm_ex(a: Quantized, b: Quantized, out=None, dtype=torch.float32, beta=0.0,
     c = out if out is not None else torch.empty(M, N, dtype=dtype, device=a.codes.device)
     nvfp4_gemm_ex(a.codes, a.scales, a.tensor_scale, b.codes, b.scales, b.tensor_scale, M, N, K, c, beta, amax)
     return c
+
+
+# ---- the gated feed-forward block -------------------------------------------
+def _ffn_sizes(x: Quantized, w: Quantized):
+    M, K = x.shape
+    rows, K2 = w.shape
+    if K != K2:
+        raise ValueError(f"K mismatch: {K} vs {K2}")
+    if rows % 2:
+        raise ValueError(f"nvfp4: w has {rows} rows, expected as many gate as up rows")
+    return M, rows // 2, K
+
+
+def gated_ffn(x: Quantized, w: Quantized, act=SILU, out=None, dtype=torch.bfloat16):
+    """h = act(a) * u, [M][F], with [a | u] = deq(x) . deq(w)^T: the first half
+    of w's rows is the gate projection, the second half the up projection."""
+    M, F, K = _ffn_sizes(x, w)
+    h = out if out is not None else torch.empty(M, F, dtype=dtype, device=x.codes.device)
+    nvfp4_gated_ffn(x.codes, x.scales, x.tensor_scale, w.codes, w.scales, w.tensor_scale, M, F, K, act, h)
+    return h
+
+
+def gated_ffn_grad(dh, x: Quantized, w: Quantized, act=SILU, out=None, amax=None):
+    """[dh u act'(a) | dh act(a)], [M][2F], for the gradient dh of gated_ffn's
+    output; when amax (a 1-element float32 device tensor) is given it receives
+    the largest magnitude stored."""
+    M, F, K = _ffn_sizes(x, w)
+    dgu = out if out is not None else torch.empty(M, 2 * F, dtype=dh.dtype, device=x.codes.device)
+    nvfp4_gated_ffn_grad(x.codes, x.scales, x.tensor_scale, w.codes, w.scales, w.tensor_scale, M, F, K, act, dh, dgu,
+                         amax)
+    return dgu
+
+
+def gated_ffn_backward(dh, x: Quantized, x_t: Quantized, w: Quantized, act=SILU, rounding=SR, seed=0, seed_t=1,
+                       rht_t=True, rht_seed=0, dtype=torch.float32):
+    """(dx [M][K], dw [2F][K]) of gated_ffn for the gradient dh [M][F] of its
+    output.  x and x_t are the two copies that quantize_cast_transpose made of
+    the input, w holds its transposed copy (quantize_2d).  The pre-activations'
+    gradient is quantized along both axes (rounding, seed, seed_t, rht_t,
+    rht_seed as in quantize_cast_transpose; x_t must have been made with the
+    same rht_t and rht_seed) and multiplied with w and x.  M % 16 == 0 and
+    F % 8 == 0, as the quantizer needs."""
+    M, F, K = _ffn_sizes(x, w)
+    if tuple(x_t.shape) != (K, M):
+        raise ValueError(f"nvfp4: x_t must be the quantization of x^T, {K} x {M}, got {tuple(x_t.shape)}")
+    if M % 16 or F % 8:
+        raise ValueError(f"nvfp4: the backward needs M % 16 == 0 and F % 8 == 0, got M = {M}, F = {F}")
+    w_t = w.transposed()
+    dev = x.codes.device
+    q, qt = _alloc(M, 2 * F, dev, False), _alloc(2 * F, M, dev, False)
+    dgu = gated_ffn_grad(dh, x, w, act, amax=q.tensor_scale[1:])
+    if rht_t:  # the transformed copy has an amax of its own
+        nvfp4_quantize_cast_transpose(dgu, rounding, seed, seed_t, 1, rht_seed, q.codes, q.scales, q.tensor_scale,
+                                      qt.codes, qt.scales, qt.tensor_scale)
+    else:
+        nvfp4_quantize_cast_transpose_with_amax(dgu, rounding, seed, seed_t, q.codes, q.scales, q.tensor_scale,
+                                                qt.codes, qt.scales, qt.tensor_scale)
+    return gemm_ex(q, w_t, dtype=dtype), gemm_ex(qt, x_t, dtype=dtype)
+
+
+# ---- distillation from a teacher's top logits ---------------------------------
+def distill_topk(logits, idx, top, weight=None, temperature=1.0):
+    """(loss [T], lse [T]) of logits [T][V] against the teacher's entries
+    idx [T][K] (int32; outside 0 .. V - 1: absent) and top [T][K] (float32)."""
+    T = logits.shape[0]
+    loss, lse = torch.empty(2, T, dtype=torch.float32, device=logits.device).unbind(0)
+    nvfp4_distill_topk(logits, idx, top, weight, temperature, loss, lse, None)
+    return loss, lse
+
+
+def distill_topk_loss_and_grad(logits, idx, top, weight=None, temperature=1.0):
+    """(loss [T], lse [T], gradient of the loss rows' sum [T][V])."""
+    T = logits.shape[0]
+    loss, lse = torch.empty(2, T, dtype=torch.float32, device=logits.device).unbind(0)
+    grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    nvfp4_distill_topk(logits, idx, top, weight, temperature, loss, lse, grad)
+    return loss, lse, grad
+
+
+def distill_topk_grad(logits, idx, top, lse, weight=None, temperature=1.0):
+    """The gradient alone, from the lse that distill_topk returned."""
+    grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    nvfp4_distill_topk(logits, idx, top, weight, temperature, None, lse, grad)
+    return grad
+
+
+# ---- embedding ------------------------------------------------------------------
+def embed(tokens, table, scale=1.0):
+    """scale * table[tokens], [T][D]; a token outside the table gives a zero row."""
+    out = torch.empty(tokens.shape[0], table.shape[1], dtype=table.dtype, device=table.device)
+    nvfp4_embed(tokens, table, scale, out)
+    return out
+
+
+def embed_grad(tokens, dout, rows, scale=1.0):
+    """The fp32 gradient [rows][D] of embed's table for the gradient dout [T][D]."""
+    grad = torch.empty(rows, dout.shape[1], dtype=torch.float32, device=dout.device)
+    nvfp4_embed_grad(tokens, dout, scale, grad)
+    return grad

@@ -69,6 +69,31 @@ int validate_quant(const void* x, int dtype, int64_t rows, int64_t cols, int rou
   return NVFP4_OK;
 }
 
+// the gated feed-forward block: dh null for the forward call
+int gated_ffn(const uint8_t* x_codes, const uint8_t* x_scales, const float* x_tensor_scale, const uint8_t* w_codes,
+              const uint8_t* w_scales, const float* w_tensor_scale, int64_t M, int64_t F, int64_t K, int act,
+              int dtype, const void* dh, void* out, float* amax, void* stream, const char* where) {
+  if (!x_codes || !x_scales || !x_tensor_scale || !w_codes || !w_scales || !w_tensor_scale || !out)
+    return NVFP4_ERR_ARG;
+  if (act != NVFP4_SILU && act != NVFP4_GELU) return NVFP4_ERR_ARG;
+  if (dtype != NVFP4_F32 && dtype != NVFP4_BF16) return NVFP4_ERR_ARG;
+  if (M <= 0 || F <= 0 || K <= 0 || K % 16 != 0) return NVFP4_ERR_SHAPE;
+  if (F > (INT64_C(1) << 30) || !size_ok(M, K) || !size_ok(2 * F, K) || !size_ok(M, 2 * F)) return NVFP4_ERR_SHAPE;
+  if (M > INT64_C(65535) * 128) return NVFP4_ERR_SHAPE;  // grid.y limit
+  const uintptr_t e = dtype == NVFP4_F32 ? 4 : 2;
+  if (!aligned(x_codes, 8) || !aligned(w_codes, 8) || !aligned(x_tensor_scale, 4) || !aligned(w_tensor_scale, 4) ||
+      !aligned(out, e) || (dh && !aligned(dh, e)) || (amax && !aligned(amax, 4)))
+    return NVFP4_ERR_ALIGN;
+  int cus = 0;
+  int st = device_cus(&cus);
+  if (st) return st;
+  nvfp4::FfnArgs p{nvfp4::GemmArgs{x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, 2 * F, K,
+                                   nullptr, nullptr, 0.0f, reinterpret_cast<unsigned*>(amax)},
+                   F, act, dtype == NVFP4_BF16, dh, out};
+  nvfp4::launch_ffn(p, cus, (hipStream_t)stream);
+  return check_launch(where);
+}
+
 }  // namespace
 
 extern "C" {
@@ -146,9 +171,27 @@ int nvfp4_quantize_cast_transpose(const void* x, int dtype, int64_t rows, int64_
   if ((st = device_cus(&cus))) return st;
   nvfp4::CastTransposeArgs a{x,      dtype == NVFP4_BF16, rows,   cols,         rounding, seed,     seed_t,
                              rht_t == 1, rht_t ? nvfp4::rht_sign_mask(rht_seed) : 0u, codes, scales,
-                             tensor_scale, codes_t, scales_t, tensor_scale_t, 0u};
+                             tensor_scale, codes_t, scales_t, tensor_scale_t, 0u, false};
   nvfp4::launch_cast_transpose(a, cus, (hipStream_t)stream);
   return check_launch("nvfp4_quantize_cast_transpose");
+}
+
+int nvfp4_quantize_cast_transpose_with_amax(const void* x, int dtype, int64_t rows, int64_t cols, int rounding,
+                                            uint64_t seed, uint64_t seed_t, uint8_t* codes, uint8_t* scales,
+                                            float* tensor_scale, uint8_t* codes_t, uint8_t* scales_t,
+                                            float* tensor_scale_t, void* stream) {
+  if (!codes_t || !tensor_scale_t) return NVFP4_ERR_ARG;
+  int st = validate_quant(x, dtype, rows, cols, rounding, codes, scales, tensor_scale, codes_t, scales_t);
+  if (st) return st;
+  if (rows % 16 != 0) return NVFP4_ERR_SHAPE;
+  if (!aligned(tensor_scale_t, 4)) return NVFP4_ERR_ALIGN;
+  int cus = 0;
+  if ((st = device_cus(&cus))) return st;
+  nvfp4::CastTransposeArgs a{x,      dtype == NVFP4_BF16, rows,         cols,    rounding, seed, seed_t,
+                             false,  0u,                  codes,        scales,  tensor_scale,
+                             codes_t, scales_t,           tensor_scale_t, 0u,    true};
+  nvfp4::launch_cast_transpose(a, cus, (hipStream_t)stream);
+  return check_launch("nvfp4_quantize_cast_transpose_with_amax");
 }
 
 int nvfp4_rht(const void* x, int dtype, int64_t rows, int64_t cols, uint64_t rht_seed, float* y,
@@ -259,6 +302,76 @@ int nvfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_t
                     0.0f,    nullptr};
   nvfp4::launch_gemm(g, cus, (hipStream_t)stream);
   return check_launch("nvfp4_gemm");
+}
+
+int nvfp4_gated_ffn(const uint8_t* x_codes, const uint8_t* x_scales, const float* x_tensor_scale,
+                    const uint8_t* w_codes, const uint8_t* w_scales, const float* w_tensor_scale, int64_t M,
+                    int64_t F, int64_t K, int act, void* h, int h_dtype, void* stream) {
+  return gated_ffn(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, act, h_dtype,
+                   nullptr, h, nullptr, stream, "nvfp4_gated_ffn");
+}
+
+int nvfp4_gated_ffn_grad(const uint8_t* x_codes, const uint8_t* x_scales, const float* x_tensor_scale,
+                         const uint8_t* w_codes, const uint8_t* w_scales, const float* w_tensor_scale, int64_t M,
+                         int64_t F, int64_t K, int act, const void* dh, void* dgu, int dtype, float* dgu_amax,
+                         void* stream) {
+  if (!dh) return NVFP4_ERR_ARG;
+  return gated_ffn(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, act, dtype, dh,
+                   dgu, dgu_amax, stream, "nvfp4_gated_ffn_grad");
+}
+
+int nvfp4_distill_topk(const void* logits, int dtype, int64_t T, int64_t V, int64_t stride, const int32_t* idx,
+                       const float* top, int64_t K, const float* weight, float temperature, float* loss, float* lse,
+                       void* grad, void* stream) {
+  if (T != 0 && (!logits || !idx || !top || !lse || (!loss && !grad))) return NVFP4_ERR_ARG;
+  if (dtype != NVFP4_F32 && dtype != NVFP4_BF16) return NVFP4_ERR_ARG;
+  if (!(temperature > 0.0f) || temperature == INFINITY) return NVFP4_ERR_ARG;
+  if (T < 0 || T >= (INT64_C(1) << 22) || V <= 0 || V >= (INT64_C(1) << 31) || K <= 0 || K > nvfp4::kDistillMaxK ||
+      stride < V || stride > (INT64_C(1) << 40) / std::max<int64_t>(T, 1))
+    return NVFP4_ERR_SHAPE;
+  const uintptr_t e = dtype == NVFP4_F32 ? 4 : 2;
+  if (!aligned(logits, e) || !aligned(idx, 4) || !aligned(top, 4) || !aligned(weight, 4) || !aligned(loss, 4) ||
+      !aligned(lse, 4) || !aligned(grad, e))
+    return NVFP4_ERR_ALIGN;
+  if (T == 0) return NVFP4_OK;
+  nvfp4::DistillArgs a{logits, dtype == NVFP4_BF16, T, V, stride, idx, top, (int)K, weight, temperature, loss, lse,
+                       grad};
+  nvfp4::launch_distill(a, (hipStream_t)stream);
+  return check_launch("nvfp4_distill_topk");
+}
+
+int nvfp4_embed(const int32_t* tokens, int64_t T, const void* table, int dtype, int64_t V, int64_t D, float scale,
+                void* out, void* stream) {
+  if (!table || (T != 0 && (!tokens || !out))) return NVFP4_ERR_ARG;
+  if (dtype != NVFP4_F32 && dtype != NVFP4_BF16) return NVFP4_ERR_ARG;
+  if (!std::isfinite(scale)) return NVFP4_ERR_ARG;
+  if (T < 0 || V <= 0 || V > (INT64_C(1) << 27) || D <= 0 || !size_ok(V, D) || !size_ok(T, D))
+    return NVFP4_ERR_SHAPE;
+  const uintptr_t e = dtype == NVFP4_F32 ? 4 : 2;
+  if (!aligned(tokens, 4) || !aligned(table, e) || !aligned(out, e)) return NVFP4_ERR_ALIGN;
+  if (T == 0) return NVFP4_OK;
+  int cus = 0;
+  int st = device_cus(&cus);
+  if (st) return st;
+  nvfp4::EmbedArgs a{tokens, T, V, D, dtype == NVFP4_BF16, scale, table, out};
+  nvfp4::launch_embed(a, cus, (hipStream_t)stream);
+  return check_launch("nvfp4_embed");
+}
+
+int nvfp4_embed_grad(const int32_t* tokens, int64_t T, const void* dout, int dtype, int64_t V, int64_t D,
+                     float scale, float* grad, void* stream) {
+  if (!grad || (T != 0 && (!tokens || !dout))) return NVFP4_ERR_ARG;
+  if (dtype != NVFP4_F32 && dtype != NVFP4_BF16) return NVFP4_ERR_ARG;
+  if (!std::isfinite(scale)) return NVFP4_ERR_ARG;
+  if (T < 0 || V <= 0 || V > (INT64_C(1) << 27) || D <= 0 || !size_ok(V, D) || !size_ok(T, D))
+    return NVFP4_ERR_SHAPE;
+  if (!aligned(tokens, 4) || !aligned(dout, dtype == NVFP4_F32 ? 4 : 2) || !aligned(grad, 4)) return NVFP4_ERR_ALIGN;
+  int cus = 0;
+  int st = device_cus(&cus);
+  if (st) return st;
+  nvfp4::EmbedArgs a{tokens, T, V, D, dtype == NVFP4_BF16, scale, dout, grad};
+  nvfp4::launch_embed_grad(a, cus, (hipStream_t)stream);
+  return check_launch("nvfp4_embed_grad");
 }
 
 }  // extern "C"

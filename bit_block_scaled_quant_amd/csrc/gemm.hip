@@ -25,167 +25,9 @@
 // v_mfma_f32_16x16x32_f16.  Lane group g = lane / 16 of a fragment covers the
 // 32 K-elements [32g, 32g+32) of a step; its word s feeds MFMA slice s.
 // k_gemm_m32 (256-multiples, below) is the fast path.
-#include "internal.hpp"
-#include "nvfp4_device.hpp"
+#include "gemm_device.hpp"
 
 namespace nvfp4 {
-
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef _Float16 half2v __attribute__((ext_vector_type(2)));
-typedef float floatx4 __attribute__((ext_vector_type(4)));
-
-constexpr int kGemmThreads = 256;  // 4 waves in a 2 x 2 grid
-constexpr int kBK = 128;           // K-elements per step
-constexpr int kRowBytes = kBK / 2;  // 64 bytes of codes per row per step
-constexpr int kRowScales = kBK / 16;
-
-template <int BM, int BN>
-struct __align__(16) GemmStage {
-  uint8_t a[BM * kRowBytes];
-  uint8_t b[BN * kRowBytes];
-  uint8_t as[BM * kRowScales];
-  uint8_t bs[BN * kRowScales];
-};
-
-// 16-byte chunk c of row r lives at chunk c ^ ((r >> 1) & 3): eight
-// consecutive rows reading the same chunk hit eight distinct bank groups
-__device__ __forceinline__ int swz(int r, int c) { return r * kRowBytes + ((c ^ ((r >> 1) & 3)) << 4); }
-
-// Eight E2M1 codes (element 2k in the low nibble of byte k) -> eight exact
-// fp16 values times the block scale, in element order.  The gfx950
-// conversion v_cvt_scalef32_pk_f16_fp4 turns one byte into two fp16 values
-// times a power-of-two scale exactly (checked for all 256 bytes); here the
-// scale is 2^8.  The E4M3 scale byte b enters as the fp16 whose bits are
-// (b & 0x7F) << 7, which is its value times 2^-8 (subnormal E4M3 bytes become
-// fp16 subnormals), so one packed multiply yields code * scale exactly: the
-// product has at most 6 significant bits and lies in [2^-10, 2688].
-//
-// The four conversions go to four registers before any multiply: written as
-// one conversion-multiply pair per byte, the compiler reused one temporary
-// register, so every multiply waited on the conversion just before it and
-// the next conversion on that multiply.
-__device__ __forceinline__ half8 unpack8(uint32_t w, half2v sc) {
-  half2v p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, 0);
-  half2v p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, 1);
-  half2v p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, 2);
-  half2v p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, 3);
-  asm volatile("" : "+v"(p0), "+v"(p1), "+v"(p2), "+v"(p3));  // all four are live at once
-  p0 = p0 * sc;
-  p1 = p1 * sc;
-  p2 = p2 * sc;
-  p3 = p3 * sc;
-  return half8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-}
-
-// E4M3 byte -> (scale * 2^-8, scale * 2^-8) as packed fp16 bits
-__device__ __forceinline__ half2v scale_h2(uint32_t byte) {
-  return __builtin_bit_cast(half2v, (byte & 0x7Fu) * 0x00800080u);
-}
-
-// ---- global -> registers -> LDS -----------------------------------------
-template <bool ALIGNED>
-__device__ __forceinline__ uint4 load_chunk(const uint8_t* __restrict__ codes, int64_t row, int64_t K,
-                                            int64_t kk) {
-  const uint8_t* p = codes + row * (K / 2) + kk / 2;
-  if (ALIGNED) return *reinterpret_cast<const uint4*>(p);
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (kk + 32 <= K) {
-    const uint2 x0 = reinterpret_cast<const uint2*>(p)[0], x1 = reinterpret_cast<const uint2*>(p)[1];
-    v = make_uint4(x0.x, x0.y, x1.x, x1.y);
-  } else if (kk + 16 <= K) {
-    const uint2 x0 = reinterpret_cast<const uint2*>(p)[0];
-    v = make_uint4(x0.x, x0.y, 0, 0);
-  }
-  return v;
-}
-
-// the 8 scale bytes of one row for K-elements [k0, k0 + 128)
-template <bool ALIGNED>
-__device__ __forceinline__ uint2 load_scales(const uint8_t* __restrict__ scales, int64_t row, int64_t K,
-                                             int64_t k0) {
-  const uint8_t* p = scales + row * (K / 16) + k0 / 16;
-  if (ALIGNED) return *reinterpret_cast<const uint2*>(p);
-  uint32_t w[2] = {0, 0};
-  for (int j = 0; j < 8; ++j)
-    if (k0 / 16 + j < K / 16) w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
-  return make_uint2(w[0], w[1]);
-}
-
-template <int BM, int BN>
-struct Staged {
-  static constexpr int kA = BM * 4 / kGemmThreads, kB = BN * 4 / kGemmThreads;
-  static constexpr int kS = (BM + BN) / kGemmThreads;  // scale rows per thread
-  uint4 a[kA], b[kB];
-  uint2 s[kS];
-};
-
-template <int BM, int BN, bool ALIGNED>
-__device__ __forceinline__ void stage_load(const GemmArgs& g, int64_t m0, int64_t n0, int64_t k0,
-                                           Staged<BM, BN>& st) {
-  const int t = threadIdx.x;
-#pragma unroll
-  for (int i = 0; i < Staged<BM, BN>::kA; ++i) {
-    const int idx = t + i * kGemmThreads;
-    const int row = idx >> 2, chunk = idx & 3;
-    const int64_t kk = k0 + chunk * 32;
-    st.a[i] = (ALIGNED || kk < g.K) ? load_chunk<ALIGNED>(g.a_codes, min(m0 + row, g.M - 1), g.K, kk)
-                                    : make_uint4(0, 0, 0, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < Staged<BM, BN>::kB; ++i) {
-    const int idx = t + i * kGemmThreads;
-    const int row = idx >> 2, chunk = idx & 3;
-    const int64_t kk = k0 + chunk * 32;
-    st.b[i] = (ALIGNED || kk < g.K) ? load_chunk<ALIGNED>(g.b_codes, min(n0 + row, g.N - 1), g.K, kk)
-                                    : make_uint4(0, 0, 0, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < Staged<BM, BN>::kS; ++i) {
-    const int r = t + i * kGemmThreads;  // rows 0..BM-1 of A, then BN rows of B
-    if (r < BM)
-      st.s[i] = load_scales<ALIGNED>(g.a_scales, min(m0 + r, g.M - 1), g.K, k0);
-    else
-      st.s[i] = load_scales<ALIGNED>(g.b_scales, min(n0 + r - BM, g.N - 1), g.K, k0);
-  }
-}
-
-// LDS position of scale byte (row r, block column c) of a BM-row operand:
-// column-major over the 8 block columns, and inside a column the rows of
-// each wave half ordered (lane row li, tile i), so that a lane reads the
-// scales of all its tiles for one column with a single 8-byte load.
-template <int BM>
-__device__ __forceinline__ int scale_pos(int r, int c) {
-  constexpr int TI = BM / 32;
-  return c * BM + (r / (BM / 2)) * (BM / 2) + (r & 15) * TI + ((r % (BM / 2)) >> 4);
-}
-
-template <int BM, int BN>
-__device__ __forceinline__ void stage_store(GemmStage<BM, BN>& sm, const Staged<BM, BN>& st) {
-  const int t = threadIdx.x;
-#pragma unroll
-  for (int i = 0; i < Staged<BM, BN>::kA; ++i) {
-    const int idx = t + i * kGemmThreads;
-    *reinterpret_cast<uint4*>(sm.a + swz(idx >> 2, idx & 3)) = st.a[i];
-  }
-#pragma unroll
-  for (int i = 0; i < Staged<BM, BN>::kB; ++i) {
-    const int idx = t + i * kGemmThreads;
-    *reinterpret_cast<uint4*>(sm.b + swz(idx >> 2, idx & 3)) = st.b[i];
-  }
-#pragma unroll
-  for (int i = 0; i < Staged<BM, BN>::kS; ++i) {
-    const int r = t + i * kGemmThreads;
-    const uint32_t w[2] = {st.s[i].x, st.s[i].y};
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const uint8_t v = (uint8_t)(w[c >> 2] >> (8 * (c & 3)));
-      if (r < BM)
-        sm.as[scale_pos<BM>(r, c)] = v;
-      else
-        sm.bs[scale_pos<BN>(r - BM, c)] = v;
-    }
-  }
-}
 
 // ---- epilogue -------------------------------------------------------------
 // One output element: v = (acc / S_a) / S_b as two multiplies by the
@@ -208,34 +50,6 @@ __device__ __forceinline__ void store_c(const GemmArgs& g, int64_t idx, float v,
   }
 }
 
-// the wave's maximum into *g.amax (float bits; non-negative floats order
-// like their bit patterns); the atomic only when it can raise the value
-__device__ __forceinline__ void amax_to(const GemmArgs& g, float m) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-  if ((threadIdx.x & 63) == 0) {
-    const unsigned bits = __float_as_uint(m);
-    if (bits > __hip_atomic_load(g.amax, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(g.amax, bits);
-  }
-}
-
-__global__ void k_zero_amax(unsigned* p) { *p = 0u; }
-
-// the T scale bytes (T = 4 or 8) a lane reads for its tiles of one block
-// column, as one 4- or 8-byte LDS read
-template <int T>
-__device__ __forceinline__ void read_scale_bytes(const uint8_t* p, uint32_t w[2]) {
-  static_assert(T == 4 || T == 8, "tiles per wave half");
-  if (T == 8) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    w[0] = x.x;
-    w[1] = x.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-    w[1] = 0u;
-  }
-}
-
 // ---- the kernel ---------------------------------------------------------
 // BM x BN tile per workgroup (256 x 256, or 128 x 128 for problems whose
 // 256 x 256 tiles would not fill the CUs), (BM/2) x (BN/2) per wave.
@@ -249,61 +63,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_gemm(GemmArgs g) {
   const int li = lane & 15, lg = lane >> 4;
 
   floatx4 acc[TI][TJ];
-#pragma unroll
-  for (int i = 0; i < TI; ++i)
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-
-  const int64_t nk = (g.K + kBK - 1) / kBK;
-  Staged<BM, BN> st;
-  stage_load<BM, BN, ALIGNED>(g, m0, n0, 0, st);
-  stage_store<BM, BN>(smem[0], st);
-  __syncthreads();
-
-  for (int64_t kt = 0; kt < nk; ++kt) {
-    const bool more = kt + 1 < nk;
-    if (more) stage_load<BM, BN, ALIGNED>(g, m0, n0, (kt + 1) * kBK, st);
-    const GemmStage<BM, BN>& sm = smem[kt & 1];
-
-    // two halves of the step: words 2h, 2h+1 of each fragment share the
-    // scale byte h (K-elements 32g + 16h .. 32g + 16h + 15)
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      uint2 qa[TI], qb[TJ];
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-        qa[i] = *reinterpret_cast<const uint2*>(sm.a + swz(wm * (BM / 2) + i * 16 + li, lg) + 8 * h);
-#pragma unroll
-      for (int j = 0; j < TJ; ++j)
-        qb[j] = *reinterpret_cast<const uint2*>(sm.b + swz(wn * (BN / 2) + j * 16 + li, lg) + 8 * h);
-      // scale bytes of block column 2g + h for all tiles of this lane
-      const uint8_t* pa = sm.as + (2 * lg + h) * BM + wm * (BM / 2) + li * TI;
-      const uint8_t* pb = sm.bs + (2 * lg + h) * BN + wn * (BN / 2) + li * TJ;
-      uint32_t wa[2], wb[2];
-      read_scale_bytes<TI>(pa, wa);
-      read_scale_bytes<TJ>(pb, wb);
-      half2v sa[TI], sb[TJ];
-#pragma unroll
-      for (int i = 0; i < TI; ++i) sa[i] = scale_h2((uint8_t)(wa[i >> 2] >> (8 * (i & 3))));
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) sb[j] = scale_h2((uint8_t)(wb[j >> 2] >> (8 * (j & 3))));
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        half8 fa[TI], fb[TJ];
-#pragma unroll
-        for (int i = 0; i < TI; ++i) fa[i] = unpack8(s ? qa[i].y : qa[i].x, sa[i]);
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) fb[j] = unpack8(s ? qb[j].y : qb[j].x, sb[j]);
-#pragma unroll
-        for (int i = 0; i < TI; ++i)
-#pragma unroll
-          for (int j = 0; j < TJ; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-      }
-    }
-    if (more) stage_store<BM, BN>(smem[(kt + 1) & 1], st);
-    __syncthreads();
-  }
+  general_tile<BM, BN, ALIGNED>(g, m0, PlainRows{g, n0}, smem, acc, wm, wn, li, lg);
 
   // epilogue: C = acc / (S_a * S_b), lane holds rows 4*lg .. 4*lg+3 of column li.
   // The loops are fully unrolled, so every accumulator index is a constant:
@@ -339,286 +99,40 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_gemm(GemmArgs g) {
   if (g.amax) amax_to(g, cmax);
 }
 
-// ---- fast path: direct-to-LDS stages, 32 x 32 x 16 MFMA, pipelined unpack --
-// For M, N multiples of 256, K a multiple of 512 and aligned operands.
-//  - A stage holds 256 K-elements of both operands (128 code bytes and 16
-//    scale bytes per row, 72 KB); two stages are double buffered in LDS.
-//  - Operand bytes go from global memory straight into LDS
-//    (global_load_lds_dwordx4, 16 bytes per lane): no staging registers and
-//    no LDS store instructions.  Code rows are 8 XOR-swizzled 16-byte
-//    chunks, so the 8 rows a wave reads at once hit distinct banks.
-//  - Four waves, one per SIMD, each own 128 x 128 of the 256 x 256 tile as
-//    4 x 4 tiles of v_mfma_f32_32x32x16_f16 (accumulators in AGPRs).
-typedef __attribute__((address_space(3))) void lds_void_t;
-typedef __attribute__((address_space(1))) void glb_void_t;
-
-constexpr int kDirBK = 256;                     // K-elements per stage
-constexpr int kDirRow = kDirBK / 2;             // 128 code bytes per row
-
-// physical 16-byte chunk of logical chunk c in row r (8 chunks per row)
-__device__ __forceinline__ int dswz(int r, int c) { return r * kDirRow + ((c ^ ((r ^ (r >> 3)) & 7)) << 4); }
-
-// Lane l feeds row l % 32 of a fragment; its lane group g = l / 32 covers the
-// NVFP4 blocks 8g .. 8g + 7 of a stage, so MFMA step t = 2p + s takes half s
-// of block 8g + p from each group (A and B use the same map, so the products
-// pair up).  A step's fragments take 32 VGPRs, which leaves room to unpack
-// step t + 1 while step t multiplies: the unpack and the LDS reads of the
-// next block are interleaved instruction by instruction with the 16 MFMAs of
-// a step (sched_group_barrier), so the vector ALU works under the matrix
-// core.  The barrier that publishes the next stage sits before a stage's
-// last step, whose MFMAs then cover the next stage's first reads and unpack.
-typedef float floatx16 __attribute__((ext_vector_type(16)));
-
-// NT = 32-column MFMA tiles per wave along N: 4 for a 256 x 256 workgroup
-// tile; 2 (256 x 128) or 1 (256 x 64) for the last, partial wave of tiles.
+// Rows m0 .. and n0 .. of whole 256 x 64 NT tiles.  Part U: A block
+// 8 * wave + U, B block 2 NT * wave + U (U < 2 NT), and with U = 0 / 1 the
+// wave's rows of A / B scales.
 template <int NT>
-struct M32 {
-  static constexpr int kBN = 64 * NT;                 // tile width
-  static constexpr int kOffB = 256 * kDirRow;         // B codes after 32 KB of A codes
-  static constexpr int kOffAS = kOffB + kBN * kDirRow;  // A scales, 4 KB
-  static constexpr int kOffBS = kOffAS + 4096;          // B scales, NT KB
-  static constexpr int kStage = kOffBS + 1024 * NT;
+struct M32Plain {
+  const GemmArgs& g;
+  int64_t m0, n0;
+
+  template <int U>
+  __device__ __forceinline__ void part(int64_t k0, uint8_t* buf) const {
+    using L = M32<NT>;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t kb = g.K / 2, ks = g.K / 16;
+    {
+      const uint8_t* a0 = g.a_codes + m0 * kb + k0 / 2;
+      const int blk = 8 * wave + U;
+      const int row = 8 * blk + (lane >> 3);
+      const int chunk = (lane & 7) ^ ((row ^ (row >> 3)) & 7);
+      const uint32_t off = (uint32_t)(row * kb + 16 * chunk);
+      __builtin_amdgcn_global_load_lds((glb_void_t*)(a0 + off), (lds_void_t*)(buf + 1024 * blk), 16, 0, 0);
+    }
+    if (U < 2 * NT) {
+      const uint8_t* b0 = g.b_codes + n0 * kb + k0 / 2;
+      const int bb = 2 * NT * wave + U, brow = 8 * bb + (lane >> 3);
+      const int bchunk = (lane & 7) ^ ((brow ^ (brow >> 3)) & 7);
+      const uint32_t boff = (uint32_t)(brow * kb + 16 * bchunk);
+      __builtin_amdgcn_global_load_lds((glb_void_t*)(b0 + boff), (lds_void_t*)(buf + L::kOffB + 1024 * bb), 16,
+                                       0, 0);
+    }
+    if (U == 0) m32_issue_scales<256>(g.a_scales + m0 * ks + k0 / 16, ks, buf + L::kOffAS);
+    if (U == 1) m32_issue_scales<64 * NT>(g.b_scales + n0 * ks + k0 / 16, ks, buf + L::kOffBS);
+  }
 };
-
-template <int NT>
-struct M32Frag { half8 a[4], b[NT]; };
-template <int NT>
-struct M32Raw { uint4 a[4], b[NT]; };  // blocks 8g + 2Q (.x, .y) and 8g + 2Q + 1 (.z, .w)
-template <int NT>
-struct M32Scales { uint4 a[2], b[(NT + 1) / 2]; };  // dword 2i + q: blocks 8g + 4q .. + 3 of tile-row i
-
-// A stage's scale bytes sit in LDS in their global order: row r's 16 bytes
-// (blocks 0 .. 15 of the stage) at 16 r.  A wave loads 64 rows with one
-// 16-byte-per-lane load (with 4-byte loads into a lane-shuffled layout a
-// stage took 4 + NT load instructions per wave instead of 1 + 1, and every
-// load instruction costs issue cycles beside the MFMAs).
-template <int ROWS>
-__device__ __forceinline__ void m32_issue_scales(const uint8_t* s0, int64_t ks, uint8_t* dst) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (64 * wave >= ROWS) return;  // wave-uniform: a 128-row operand takes two waves
-  const uint32_t off = (uint32_t)((64 * wave + lane) * ks);
-  __builtin_amdgcn_global_load_lds((glb_void_t*)(s0 + off), (lds_void_t*)(dst + 1024 * wave), 16, 0, 0);
-}
-
-// Part U (0..7) of a stage's loads: A block 8 * wave + U, B block
-// 2 NT * wave + U (U < 2 NT), and with U = 0 / 1 the wave's rows of A / B
-// scales.  A stage is issued as eight such parts spread over the
-// first four step pairs: issued all at once, the 24 loads of every wave
-// backed up in the texture unit and stalled the waves' MFMA issue (about 57
-// cycles per load instruction, by counters).
-template <int NT, int U>
-__device__ __forceinline__ void m32_issue_part(const GemmArgs& g, int64_t m0, int64_t n0, int64_t k0,
-                                               uint8_t* buf) {
-  using L = M32<NT>;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t kb = g.K / 2, ks = g.K / 16;
-  {
-    const uint8_t* a0 = g.a_codes + m0 * kb + k0 / 2;
-    const int blk = 8 * wave + U;
-    const int row = 8 * blk + (lane >> 3);
-    const int chunk = (lane & 7) ^ ((row ^ (row >> 3)) & 7);
-    const uint32_t off = (uint32_t)(row * kb + 16 * chunk);
-    __builtin_amdgcn_global_load_lds((glb_void_t*)(a0 + off), (lds_void_t*)(buf + 1024 * blk), 16, 0, 0);
-  }
-  if (U < 2 * NT) {
-    const uint8_t* b0 = g.b_codes + n0 * kb + k0 / 2;
-    const int bb = 2 * NT * wave + U, brow = 8 * bb + (lane >> 3);
-    const int bchunk = (lane & 7) ^ ((brow ^ (brow >> 3)) & 7);
-    const uint32_t boff = (uint32_t)(brow * kb + 16 * bchunk);
-    __builtin_amdgcn_global_load_lds((glb_void_t*)(b0 + boff), (lds_void_t*)(buf + L::kOffB + 1024 * bb), 16,
-                                     0, 0);
-  }
-  if (U == 0) m32_issue_scales<256>(g.a_scales + m0 * ks + k0 / 16, ks, buf + L::kOffAS);
-  if (U == 1) m32_issue_scales<64 * NT>(g.b_scales + n0 * ks + k0 / 16, ks, buf + L::kOffBS);
-}
-
-template <int NT>
-__device__ __forceinline__ void m32_issue(const GemmArgs& g, int64_t m0, int64_t n0, int64_t k0,
-                                          uint8_t* buf) {
-  m32_issue_part<NT, 0>(g, m0, n0, k0, buf);
-  m32_issue_part<NT, 1>(g, m0, n0, k0, buf);
-  m32_issue_part<NT, 2>(g, m0, n0, k0, buf);
-  m32_issue_part<NT, 3>(g, m0, n0, k0, buf);
-  m32_issue_part<NT, 4>(g, m0, n0, k0, buf);
-  m32_issue_part<NT, 5>(g, m0, n0, k0, buf);
-  m32_issue_part<NT, 6>(g, m0, n0, k0, buf);
-  m32_issue_part<NT, 7>(g, m0, n0, k0, buf);
-}
-
-template <int NT>
-__device__ __forceinline__ void m32_read_scales(const uint8_t* buf, int wm, int wn, int r, int gq,
-                                                M32Scales<NT>& d) {
-  using L = M32<NT>;
-  // tile-row i of A is row wm * 128 + 32 i + r; lane group gq takes blocks
-  // 8 gq .. 8 gq + 7, i.e. bytes 8 gq .. 8 gq + 7 of the row (a read
-  // instruction covers 512 contiguous bytes: no bank conflicts)
-  const uint8_t* pa = buf + L::kOffAS + 16 * (wm * 128 + r) + 8 * gq;
-  const uint8_t* pb = buf + L::kOffBS + 16 * (wn * 32 * NT + r) + 8 * gq;
-  uint2 ra[4], rb[NT];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) ra[i] = *reinterpret_cast<const uint2*>(pa + 16 * 32 * i);
-#pragma unroll
-  for (int j = 0; j < NT; ++j) rb[j] = *reinterpret_cast<const uint2*>(pb + 16 * 32 * j);
-  d.a[0] = make_uint4(ra[0].x, ra[0].y, ra[1].x, ra[1].y);
-  d.a[1] = make_uint4(ra[2].x, ra[2].y, ra[3].x, ra[3].y);
-#pragma unroll
-  for (int k = 0; k < (NT + 1) / 2; ++k) {
-    const uint2 hi = 2 * k + 1 < NT ? rb[2 * k + 1 < NT ? 2 * k + 1 : 0] : make_uint2(0u, 0u);
-    d.b[k] = make_uint4(rb[2 * k].x, rb[2 * k].y, hi.x, hi.y);
-  }
-}
-
-// raw codes of blocks 8g + 2Q and 8g + 2Q + 1 (one 16-byte chunk) for the
-// lane's four A and NT B rows; the eight rows of a swizzle group hit eight
-// distinct chunk positions, so a 16-byte read is free of bank conflicts
-template <int Q, int NT>
-__device__ __forceinline__ void m32_read_raw(const uint8_t* buf, int wm, int wn, int r, int gq,
-                                             M32Raw<NT>& q) {
-  const int c = 4 * gq + Q;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) q.a[i] = *reinterpret_cast<const uint4*>(buf + dswz(wm * 128 + i * 32 + r, c));
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-    q.b[j] = *reinterpret_cast<const uint4*>(buf + M32<NT>::kOffB + dswz(wn * 32 * NT + j * 32 + r, c));
-}
-
-__device__ __forceinline__ uint32_t raw_word(const uint4& v, int k) {
-  return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
-}
-
-__device__ __forceinline__ uint32_t m32_dword(const uint4& v0, const uint4& v1, int k) {
-  return k == 0 ? v0.x : k == 1 ? v0.y : k == 2 ? v0.z : k == 3 ? v0.w : k == 4 ? v1.x : k == 5 ? v1.y
-       : k == 6 ? v1.z : v1.w;
-}
-
-// step (P, S): half S of block 8g + P
-template <int P, int S, int NT>
-__device__ __forceinline__ void m32_unpack(const M32Raw<NT>& q, const M32Scales<NT>& d, M32Frag<NT>& f) {
-  constexpr int kw = 2 * (P & 1) + S;  // word of the 16-byte chunk
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    f.a[i] = unpack8(raw_word(q.a[i], kw),
-                     scale_h2(m32_dword(d.a[0], d.a[1], 2 * i + (P >> 2)) >> (8 * (P & 3))));
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-    f.b[j] = unpack8(raw_word(q.b[j], kw),
-                     scale_h2(m32_dword(d.b[0], d.b[(NT + 1) / 2 - 1], 2 * j + (P >> 2)) >> (8 * (P & 3))));
-}
-
-template <int NT>
-__device__ __forceinline__ void m32_mfma(const M32Frag<NT>& f, floatx16 (&acc)[4][NT]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
-}
-
-// Instruction order of one step of 4 NT MFMAs; READS groups of LDS reads ride
-// on the first MFMAs; with DEP the unpack waits on them behind a few MFMAs.
-// A step's unpack is about 10 VALU per fragment (4 + NT fragments).
-template <int READS, bool DEP, int NT>
-__device__ __forceinline__ void m32_order() {
-  constexpr int kMfma = 4 * NT;
-#pragma unroll
-  for (int k = 0; k < READS; ++k) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, DEP ? 2 : 1, 0);
-    if (!DEP) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-  }
-  constexpr int kCover = DEP ? (NT == 4 ? 3 : 2) : 0;
-#pragma unroll
-  for (int k = 0; k < kCover; ++k) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-  constexpr int kRest = kMfma - READS - kCover;
-  constexpr int kValu = NT == 4 ? (DEP ? 8 : 5) : (DEP ? 14 : 7);  // group sizes tuned by measurement
-#pragma unroll
-  for (int k = 0; k < kRest; ++k) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, kValu, 0);
-  }
-}
-
-// pair P of a stage: steps 2P and 2P + 1.  In: f = step (P, 0), q = raw of
-// quad P / 2 (pairs P & ~1 and P | 1).  An even pair also reads the next
-// quad into qn; an odd pair hands it over.
-template <int P, int NT>
-__device__ __forceinline__ void m32_pair(const uint8_t* cur, M32Frag<NT>& f, M32Raw<NT>& q, M32Raw<NT>& qn,
-                                         const M32Scales<NT>& d, floatx16 (&acc)[4][NT], int wm, int wn,
-                                         int r, int gq) {
-  constexpr bool kRead = (P & 1) == 0 && P < 6;
-  M32Frag<NT> f1;
-  m32_mfma<NT>(f, acc);
-  if (kRead) m32_read_raw<P / 2 + 1, NT>(cur, wm, wn, r, gq, qn);
-  m32_unpack<P, 1, NT>(q, d, f1);
-  m32_order<kRead ? 4 + NT : 0, false, NT>();
-  __builtin_amdgcn_sched_barrier(0);
-  m32_mfma<NT>(f1, acc);
-  if (P & 1) {
-    m32_unpack<P + 1, 0, NT>(qn, d, f);
-    q = qn;
-  } else {
-    m32_unpack<P + 1, 0, NT>(q, d, f);
-  }
-  m32_order<0, false, NT>();
-  __builtin_amdgcn_sched_barrier(0);
-}
-
-// One stage from cur.  In: f = step (0, 0), q = raw 0, d = scales.  Out: the
-// same for the stage in nxt.  When issue is set, the stage at (m0, n0,
-// k_issue) streams into nxt after the first pair of steps: every wave passed
-// the barrier that ended the previous stage, the last reader of nxt.  The
-// barrier before the last step waits for those loads.  No load is then in
-// flight at a loop back edge, where the compiler's wait insertion would
-// otherwise make the first LDS reads of cur wait for the loads into nxt.
-template <int NT>
-__device__ __forceinline__ void m32_stage(const GemmArgs& g, int64_t m0, int64_t n0, bool issue,
-                                          int64_t k_issue, const uint8_t* cur, uint8_t* nxt, M32Frag<NT>& f,
-                                          M32Raw<NT>& q, M32Scales<NT>& d, floatx16 (&acc)[4][NT], int wm,
-                                          int wn, int r, int gq) {
-  M32Raw<NT> qn;
-  m32_pair<0, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
-  if (issue) {
-    m32_issue_part<NT, 0>(g, m0, n0, k_issue, nxt);
-    m32_issue_part<NT, 1>(g, m0, n0, k_issue, nxt);
-  }
-  __builtin_amdgcn_sched_barrier(0);
-  m32_pair<1, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
-  if (issue) {
-    m32_issue_part<NT, 2>(g, m0, n0, k_issue, nxt);
-    m32_issue_part<NT, 3>(g, m0, n0, k_issue, nxt);
-  }
-  __builtin_amdgcn_sched_barrier(0);
-  m32_pair<2, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
-  if (issue) {
-    m32_issue_part<NT, 4>(g, m0, n0, k_issue, nxt);
-    m32_issue_part<NT, 5>(g, m0, n0, k_issue, nxt);
-  }
-  __builtin_amdgcn_sched_barrier(0);
-  m32_pair<3, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
-  if (issue) {
-    m32_issue_part<NT, 6>(g, m0, n0, k_issue, nxt);
-    m32_issue_part<NT, 7>(g, m0, n0, k_issue, nxt);
-  }
-  __builtin_amdgcn_sched_barrier(0);
-  m32_pair<4, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
-  m32_pair<5, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
-  m32_pair<6, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
-  M32Frag<NT> f1;
-  m32_mfma<NT>(f, acc);
-  m32_unpack<7, 1, NT>(q, d, f1);
-  m32_order<0, false, NT>();
-  __builtin_amdgcn_sched_barrier(0);
-  __syncthreads();  // waits for this wave's loads of nxt (vmcnt(0)), then all waves
-  __builtin_amdgcn_sched_barrier(0);
-  m32_mfma<NT>(f1, acc);
-  m32_read_scales<NT>(nxt, wm, wn, r, gq, d);
-  m32_read_raw<0, NT>(nxt, wm, wn, r, gq, q);
-  m32_unpack<0, 0, NT>(q, d, f);
-  m32_order<NT == 4 ? 6 : 5, true, NT>();
-  __builtin_amdgcn_sched_barrier(0);
-}
 
 // Tiles are numbered in band order: bands of four tile rows, walked column
 // by column (u -> tile_mn), so that 32 consecutive tiles form a 4 x 8 block.
@@ -669,7 +183,8 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_gemm_m32(GemmArgs g, int64_
       for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.f;
 
   const int64_t nk = g.K / kDirBK;  // even
-  m32_issue<NT>(g, m0, n0, 0, buf0);
+  const M32Plain<NT> ld{g, m0, n0};
+  m32_issue(ld, 0, buf0);
   __syncthreads();
   M32Frag<NT> f;
   M32Raw<NT> q;
@@ -678,9 +193,9 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_gemm_m32(GemmArgs g, int64_
   m32_read_raw<0, NT>(buf0, wm, wn, r, gq, q);
   m32_unpack<0, 0, NT>(q, d, f);
   for (int64_t kt = 0; kt < nk; kt += 2) {
-    m32_stage<NT>(g, m0, n0, true, (kt + 1) * kDirBK, buf0, buf1, f, q, d, acc, wm, wn, r, gq);
+    m32_stage<NT>(ld, true, (kt + 1) * kDirBK, buf0, buf1, f, q, d, acc, wm, wn, r, gq);
     // on the last stage the reads of buf0 at its end are of stale data and unused
-    m32_stage<NT>(g, m0, n0, kt + 2 < nk, (kt + 2) * kDirBK, buf1, buf0, f, q, d, acc, wm, wn, r, gq);
+    m32_stage<NT>(ld, kt + 2 < nk, (kt + 2) * kDirBK, buf1, buf0, f, q, d, acc, wm, wn, r, gq);
   }
 
   // D layout of the 32 x 32 MFMA: lane l, value k -> column l % 32, row
@@ -839,9 +354,13 @@ static void launch_m32(const GemmArgs& g, int64_t ntiles, int64_t full, int64_t 
   }
 }
 
+__global__ void k_zero_amax(unsigned* p) { *p = 0u; }
+
+void launch_zero_amax(unsigned* p, hipStream_t st) { hipLaunchKernelGGL(k_zero_amax, dim3(1), dim3(1), 0, st, p); }
+
 void launch_gemm(const GemmArgs& g, int cus, hipStream_t st) {
   constexpr int BM = 256, BN = 256;
-  if (g.amax) hipLaunchKernelGGL(k_zero_amax, dim3(1), dim3(1), 0, st, g.amax);
+  if (g.amax) launch_zero_amax(g.amax, st);
   const dim3 grid((unsigned)((g.N + BN - 1) / BN), (unsigned)((g.M + BM - 1) / BM));
   const bool aligned = g.K % kBK == 0 && ((uintptr_t)g.a_codes % 16 == 0) &&
                        ((uintptr_t)g.b_codes % 16 == 0) && ((uintptr_t)g.a_scales % 8 == 0) &&

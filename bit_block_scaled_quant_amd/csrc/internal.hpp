@@ -44,6 +44,7 @@ struct CastTransposeArgs {
   uint8_t* scales_t;
   float* tensor_scale_t;  // may equal tensor_scale when rht_t is off
   uint32_t stream_t;      // SR stream of the columnwise copy: 0, or 1 for nvfp4_quantize's copy
+  bool amax_given;        // tensor_scale[1] already holds the amax (no transform): skip pass 1
 };
 
 void launch_cast_transpose(const CastTransposeArgs& a, int cus, hipStream_t st);
@@ -67,6 +68,52 @@ struct GemmArgs {
 };
 
 void launch_gemm(const GemmArgs& g, int cus, hipStream_t st);
+void launch_zero_amax(unsigned* p, hipStream_t st);  // *p = 0 (a kernel: captures into graphs)
+
+// Gated feed-forward block: [a | u] = deq(X) . deq(W)^T with W's first F rows
+// the gate's and its last F rows the up projection's
+struct FfnArgs {
+  GemmArgs g;        // a: X [M][K], b: W [2F][K], N = 2F; g.amax: max |stored gradient|
+  int64_t F;
+  int act;           // 0 SiLU, 1 GELU (tanh form)
+  bool bf16;         // type of dh and out
+  const void* dh;    // [M][F]: out = [dh u act'(a) | dh act(a)], [M][2F]; null:
+  void* out;         // out = act(a) u, [M][F]
+};
+
+void launch_ffn(const FfnArgs& a, int cus, hipStream_t st);
+
+// Distillation from a teacher's top logits
+struct DistillArgs {
+  const void* logits;  // [T][V], rows `stride` elements apart
+  bool bf16;
+  int64_t T, V, stride;
+  const int32_t* idx;  // [T][K]; entries outside 0 .. V - 1 are absent
+  const float* top;    // [T][K]
+  int K;
+  const float* weight;  // [T] or null (all ones)
+  float temperature;
+  float* loss;          // [T], or null (gradient alone, from the given lse)
+  float* lse;           // [T]
+  void* grad;           // [T][V] contiguous, type of the logits, or null (loss alone)
+};
+
+constexpr int kDistillMaxK = 1024;
+
+void launch_distill(const DistillArgs& a, hipStream_t st);
+
+// Embedding lookup and the gradient of its table
+struct EmbedArgs {
+  const int32_t* tok;  // [T]; outside 0 .. V - 1: a zero row, no gradient
+  int64_t T, V, D;
+  bool bf16;           // type of table and out, or of dout
+  float scale;
+  const void* in;      // table [V][D], or dout [T][D]
+  void* out;           // [T][D], or the fp32 gradient [V][D]
+};
+
+void launch_embed(const EmbedArgs& a, int cus, hipStream_t st);
+void launch_embed_grad(const EmbedArgs& a, int cus, hipStream_t st);
 
 // MXFP4: 32-element blocks of E2M1 codes with E8M0 (power-of-two) scales
 struct MxGemmArgs {

@@ -796,14 +796,14 @@ static void launch_tile(const QuantArgs& a, bool two_d, int cus, hipStream_t st)
     // every element encoded once from the rowwise draws
     CastTransposeArgs c{a.x,     a.bf16,   a.rows,         a.cols,  a.rounding, a.seed, a.seed,
                         false,   0u,       a.codes,        a.scales, a.tensor_scale, a.codes_t, a.scales_t,
-                        a.tensor_scale, 0u};
+                        a.tensor_scale, 0u, true};
     launch_ct_encode<BF16, SR, false, true>(c, cus, st);
   } else {
     // 1D with the columnwise copy: the cast-transpose encoder with one tensor
     // scale for both copies and the columnwise SR draws from stream 1 of seed
     CastTransposeArgs c{a.x,     a.bf16,   a.rows,         a.cols,  a.rounding, a.seed, a.seed,
                         false,   0u,       a.codes,        a.scales, a.tensor_scale, a.codes_t, a.scales_t,
-                        a.tensor_scale, 1u};
+                        a.tensor_scale, 1u, true};
     launch_ct_encode<BF16, SR, false>(c, cus, st);
   }
 }
@@ -877,11 +877,13 @@ static void launch_cast_transpose_t(const CastTransposeArgs& a, int cus, hipStre
     else
       launch_ct_encode<BF16, false, true>(a, cus, st);
   } else {
-    hipLaunchKernelGGL(k_init_amax, dim3(1), dim3(1), 0, st, a.tensor_scale);
-    if (amax_cached(a.rows, a.cols, BF16))
-      launch_amax_plain<BF16, true>(a.x, a.rows * a.cols, a.tensor_scale, cus, st);
-    else
-      launch_amax_plain<BF16, false>(a.x, a.rows * a.cols, a.tensor_scale, cus, st);
+    if (!a.amax_given) {
+      hipLaunchKernelGGL(k_init_amax, dim3(1), dim3(1), 0, st, a.tensor_scale);
+      if (amax_cached(a.rows, a.cols, BF16))
+        launch_amax_plain<BF16, true>(a.x, a.rows * a.cols, a.tensor_scale, cus, st);
+      else
+        launch_amax_plain<BF16, false>(a.x, a.rows * a.cols, a.tensor_scale, cus, st);
+    }
     if (sr)
       launch_ct_encode<BF16, true, false>(a, cus, st);
     else

@@ -69,6 +69,7 @@ enum nvfp4_status {
 
 enum nvfp4_dtype { NVFP4_F32 = 0, NVFP4_BF16 = 1 };
 enum nvfp4_rounding { NVFP4_RNE = 0, NVFP4_SR = 1 };
+enum nvfp4_activation { NVFP4_SILU = 0, NVFP4_GELU = 1 /* tanh form */ };
 
 /*
  * 1D NVFP4 quantization of x [rows][cols] (row-major, dtype f32 or bf16)
@@ -253,6 +254,94 @@ int nvfp4_gemm_ex(const uint8_t* a_codes, const uint8_t* a_scales, const float* 
 int nvfp4_quantize_with_amax(const void* x, int dtype, int64_t rows, int64_t cols, int rounding,
                              uint64_t seed, int rht, uint64_t rht_seed, uint8_t* codes,
                              uint8_t* scales, float* tensor_scale, void* stream);
+
+/*
+ * nvfp4_quantize_cast_transpose(rht_t = 0) without its first pass:
+ * tensor_scale[1] must already hold the amax of x (e.g. the dgu_amax of
+ * nvfp4_gated_ffn_grad).  With that amax all six outputs are bit-identical,
+ * from a single read of x.  Arguments otherwise as there.
+ */
+int nvfp4_quantize_cast_transpose_with_amax(const void* x, int dtype, int64_t rows, int64_t cols, int rounding,
+                                            uint64_t seed, uint64_t seed_t, uint8_t* codes, uint8_t* scales,
+                                            float* tensor_scale, uint8_t* codes_t, uint8_t* scales_t,
+                                            float* tensor_scale_t, void* stream);
+
+/*
+ * Gated feed-forward block: with [a | u] = deq(X) . deq(W)^T, X an NVFP4 tensor
+ * of M x K and W one of 2F x K (rows 0 .. F - 1 the gate's, F .. 2F - 1 the up
+ * projection's), both quantized along K,
+ *   h [M][F] = act(a) u,
+ * act = NVFP4_SILU a / (1 + e^-a), or NVFP4_GELU a (1 + tanh z) / 2 with
+ * z = sqrt(2 / pi) (a + 0.044715 a^3).  The products are computed as
+ * nvfp4_gemm's; activation and product are fp32, and h is that value (h_dtype
+ * NVFP4_F32) or the value rounded to nearest-even bf16 (NVFP4_BF16).
+ * Shapes: M, F >= 1, K >= 16, K % 16 == 0, F <= 2^30, M at most 65535 * 128.
+ * Alignment: codes 8 bytes, h one element, tensor scales 4 bytes.
+ */
+int nvfp4_gated_ffn(const uint8_t* x_codes, const uint8_t* x_scales, const float* x_tensor_scale,
+                    const uint8_t* w_codes, const uint8_t* w_scales, const float* w_tensor_scale, int64_t M,
+                    int64_t F, int64_t K, int act, void* h, int h_dtype, void* stream);
+
+/*
+ * The gradient of its two pre-activations, recomputed from X and W, for the
+ * gradient dh [M][F] of h:
+ *   dgu [M][2F] = [dh u act'(a) | dh act(a)],
+ * the layout of W's rows, so that dX = dgu . deq(W) and dW = dgu^T . deq(X)
+ * are one product each.  dh and dgu have one dtype.
+ *   dgu_amax (NULL or a device float): set to max |stored dgu|, for
+ *   nvfp4_quantize_cast_transpose_with_amax.
+ * Shapes and alignment as nvfp4_gated_ffn; dh one element, dgu_amax 4 bytes.
+ */
+int nvfp4_gated_ffn_grad(const uint8_t* x_codes, const uint8_t* x_scales, const float* x_tensor_scale,
+                         const uint8_t* w_codes, const uint8_t* w_scales, const float* w_tensor_scale, int64_t M,
+                         int64_t F, int64_t K, int act, const void* dh, void* dgu, int dtype, float* dgu_amax,
+                         void* stream);
+
+/*
+ * Distillation from a teacher's top logits.  For row r of logits (T rows of V,
+ * `stride` >= V elements apart), z = logits / temperature and the entries
+ * (idx [T][K], top [T][K]) of the teacher:
+ *   lse_r  = log sum_v exp(z_v),
+ *   p      = softmax over the row's present entries of top / temperature,
+ *   loss_r = w_r sum_j p_j (log p_j - (z_idx_j - lse_r)),
+ *   grad_r = (exp(z - lse_r) - sum_j p_j e_idx_j) w_r / temperature,
+ * w = weight [T] (NULL: ones).  An entry is absent when its idx is outside
+ * 0 .. V - 1 or its top is -inf; a row with weight 0 or without entries has
+ * loss and gradient 0, whatever its logits.  Logits may be -inf (masked:
+ * gradient 0); a row of nothing else has lse -inf and loss +inf.  A NaN or
+ * +inf makes its row's results NaN.
+ *   loss, lse given, grad NULL      loss alone;
+ *   loss, lse, grad given           loss and gradient;
+ *   loss NULL, lse, grad given      gradient alone: lse is an input, as an
+ *                                   earlier call left it.
+ * grad [T][V] is contiguous and has the logits' dtype; loss, lse [T] are fp32.
+ * Shapes: 0 <= T < 2^22, 1 <= V < 2^31, 1 <= K <= 1024 (T = 0 enqueues
+ * nothing, and its buffers may be NULL).  temperature is positive and finite.
+ * Alignment: one element.
+ */
+int nvfp4_distill_topk(const void* logits, int dtype, int64_t T, int64_t V, int64_t stride, const int32_t* idx,
+                       const float* top, int64_t K, const float* weight, float temperature, float* loss, float* lse,
+                       void* grad, void* stream);
+
+/*
+ * Embedding lookup: out [T][D] = scale * table[tokens[t]] (fp32 product, bf16
+ * rounded to nearest-even), table [V][D] and out of one dtype.  A token
+ * outside 0 .. V - 1 (padding) gives a zero row.
+ * Shapes: T >= 0 (0: nothing is enqueued, tokens and out may be NULL),
+ * 1 <= V <= 2^27, D >= 1; scale is finite.  Alignment: one element.
+ */
+int nvfp4_embed(const int32_t* tokens, int64_t T, const void* table, int dtype, int64_t V, int64_t D, float scale,
+                void* out, void* stream);
+
+/*
+ * Its gradient: grad [V][D] fp32, grad[v] = scale * sum of dout[t] over the t
+ * with tokens[t] == v, zeros for a row no token names (every row is written).
+ * Sums are fp32 in one fixed order, so results repeat bit for bit.  Tokens
+ * outside 0 .. V - 1 add nothing.  With T = 0 tokens and dout may be NULL.
+ * Shapes and alignment as nvfp4_embed; dout [T][D] of `dtype`.
+ */
+int nvfp4_embed_grad(const int32_t* tokens, int64_t T, const void* dout, int dtype, int64_t V, int64_t D,
+                     float scale, float* grad, void* stream);
 
 /* Static text for a status code. */
 const char* nvfp4_status_string(int status);

@@ -1,0 +1,227 @@
+"""GPU checks of the distillation loss and its gradient against the definition
+in 64 bits.
+
+Tolerance (eps = 2^-24, all statistics fp32).  An exponent's argument x is off
+by at most 4 eps (|x| + max|z|): the difference to the maximum or to lse, the
+temperature, the product with log2 e, and lse's own rounding.  A sum of V
+exponentials adds V / 1024 + 32 roundings (1024 threads, then a tree), the
+exponential and logarithm two ulps.  So with A = max|z| + max|z - lse| over the
+finite entries, q, p and lse are good to r = eps (8 A + V / 1024 + 64),
+relative for q and p, absolute for lse.  Outputs are rounded once more: half a
+step of their type."""
+import math
+
+import pytest
+import torch
+
+import bit_block_scaled_quant_amd as nv
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+EPS = 2.0 ** -24
+
+
+def definition(logits, idx, top, weight, tau):
+    z = logits.double() / tau
+    V = z.shape[1]
+    lse = torch.logsumexp(z, 1)
+    there = (idx >= 0) & (idx < V)
+    t = (top.double() / tau).masked_fill(~there, -math.inf)
+    there = t > -math.inf
+    any_ = there.any(1)
+    high = t.amax(1, keepdim=True).masked_fill(~any_[:, None], 0.0)
+    p = torch.exp(t - high)
+    total = p.sum(1, keepdim=True)
+    logp = t - high - torch.log(total)
+    p = torch.where(any_[:, None], p / total, torch.zeros_like(p))
+    w = (torch.ones_like(lse) if weight is None else weight.double()) * any_
+    at = idx.long().clamp(0, V - 1)
+    zt = z.gather(1, at)
+    on = there & (w != 0)[:, None]
+    term = torch.where(on & (p > 0), p * (logp - (zt - lse[:, None])), torch.zeros_like(p))
+    loss = torch.where(w != 0, term.sum(1) * w, torch.zeros_like(w))
+    q = torch.exp(z - lse[:, None])
+    g = (q - torch.zeros_like(z).scatter_add_(1, at, p * there)) * (w / tau)[:, None]
+    g = torch.where((w != 0)[:, None], g, torch.zeros_like(g))
+    # tolerances
+    fin = torch.isfinite(z)
+    A = torch.where(fin, z.abs() + (z - lse[:, None]).abs(), torch.zeros_like(z)).amax(1)
+    tf = torch.where(there, (t - high).abs() + t.abs(), torch.zeros_like(t)).amax(1)
+    r = EPS * (8 * (A + tf) + V / 1024 + 64)
+    d_lse = r + EPS * lse.abs()
+    zf = torch.where(on & torch.isfinite(zt), zt.abs(), torch.zeros_like(zt))
+    d_loss = w.abs() * ((torch.where(on, p * (logp.abs() + zf + lse.abs()[:, None] + 2), torch.zeros_like(p))).sum(1) * r
+                        + r + d_lse)
+    tgt = torch.zeros_like(z).scatter_add_(1, at, p * there)
+    d_g = (q + tgt) * (w.abs() / tau * r * 2)[:, None]
+    return loss, lse, g, d_loss, d_lse, d_g
+
+
+def close(got, want, tol, what):
+    tol = tol + torch.finfo(got.dtype).eps / 2 * (want.abs() + tol) + 1e-37
+    got = got.double()
+    same = (got == want) | ((got - want).abs() <= tol)  # == for infinities
+    assert same.all(), f"{what}: {got[~same][:4].tolist()} vs {want[~same][:4].tolist()}"
+
+
+def check(logits, idx, top, weight=None, tau=1.0):
+    loss, lse, g, d_loss, d_lse, d_g = definition(logits, idx, top, weight, tau)
+    got = nv.distill_topk_loss_and_grad(logits, idx, top, weight=weight, temperature=tau)
+    alone = nv.distill_topk(logits, idx, top, weight=weight, temperature=tau)
+    for a in (got, alone):
+        close(a[1], lse, d_lse, "lse")
+        close(a[0], loss, d_loss, "loss")
+    assert got[2].dtype == logits.dtype and got[2].is_contiguous()
+    close(got[2], g, d_g, "grad")
+    # from a given lse: its rounding to fp32 moves q by its absolute error
+    d = d_g + ((d_lse + EPS * lse.abs())[:, None] * (g.abs() + d_g) * 2).nan_to_num(0.0)
+    alone = nv.distill_topk_grad(logits, idx, top, got[1], weight=weight, temperature=tau)
+    at = idx.long().clamp(0, logits.shape[1] - 1)
+    d = d.scatter_add(1, at, ((d_lse + EPS * lse.abs()) * 2 / tau).nan_to_num(0.0)[:, None].expand(at.shape).contiguous())
+    close(alone, g, d, "grad from lse")
+    again = nv.distill_topk_loss_and_grad(logits, idx, top, weight=weight, temperature=tau)
+    for a, b in zip(got, again):
+        assert torch.equal(a.view(torch.int16 if a.dtype == torch.bfloat16 else torch.int32),
+                           b.view(torch.int16 if b.dtype == torch.bfloat16 else torch.int32))
+
+
+def inputs(T, V, K, dtype, seed=0, spread=2.5):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    logits = (spread * torch.randn(T, V, generator=g, device=DEV)).to(dtype)
+    idx = torch.stack([torch.randperm(V, generator=g, device=DEV)[:K] if K <= V else
+                       torch.randint(0, V, (K,), generator=g, device=DEV) for _ in range(T)]).int()
+    top = 2 * torch.randn(T, K, generator=g, device=DEV) + 4
+    weight = torch.rand(T, generator=g, device=DEV)
+    return logits, idx, top, weight
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V,K", [(1, 1, 1), (1, 2, 1), (3, 7, 3), (2, 8, 4), (5, 9, 9), (4, 63, 1), (3, 1000, 20),
+                                   (2, 1023, 5), (2, 1025, 128), (7, 4099, 17), (3, 8191, 64), (2, 8193, 64),
+                                   (2, 16384, 33), (5, 32000, 20), (2, 50021, 100), (2, 65537, 3), (3, 131072, 64),
+                                   (1, 262147, 8), (2, 2000, 1024), (3, 5, 40)])
+def test_shapes(T, V, K, dtype):
+    check(*inputs(T, V, K, dtype, seed=V))
+
+
+@pytest.mark.parametrize("tau", [0.25, 0.7, 2.0, 16.0])
+def test_temperature(tau):
+    check(*inputs(6, 3001, 12, torch.float32, seed=4), tau=tau)
+    check(*inputs(6, 3000, 12, torch.bfloat16, seed=4), tau=tau)
+
+
+def test_many_rows():
+    check(*inputs(700, 1531, 10, torch.bfloat16, seed=5))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_masks(dtype):
+    logits, idx, top, weight = inputs(12, 2051, 16, dtype, seed=6)
+    logits[:, 1900:] = -math.inf                 # a masked tail
+    idx %= 1900
+    logits[1, :1000] = -math.inf                 # the row's first vectors hold nothing
+    logits[2] = -math.inf
+    logits[2, 1234] = 3.0                        # one entry left
+    idx[2] = -1
+    idx[2, 5] = 1234
+    logits[3] = torch.finfo(dtype).min           # the type's lowest value everywhere
+    logits[4, :1900] = torch.finfo(dtype).min    # and but for one entry
+    logits[4, 7] = 0.0
+    idx[4] = 7
+    idx[5] = -1                                  # no entry
+    idx[6, ::2] = -1
+    idx[7, ::3] = 2051                           # outside above
+    idx[7, 1::3] = 2 ** 31 - 1
+    top[8, 3:] = -math.inf                       # entries of probability zero
+    top[9] = -math.inf                           # and nothing else
+    weight[10] = 0.0
+    check(logits, idx, top, weight)
+
+
+def test_lowest_value_overflows_with_the_temperature():
+    logits, idx, top, weight = inputs(4, 777, 5, torch.float32, seed=8)
+    logits[:, 300:] = torch.finfo(torch.float32).min
+    idx %= 300
+    check(logits, idx, top, weight, tau=0.5)
+
+
+def test_masked_teacher_entry():  # the student rules out what the teacher names: infinite loss, finite gradient
+    logits, idx, top, weight = inputs(3, 500, 4, torch.float32, seed=9)
+    logits[1, idx[1, 0].long()] = -math.inf
+    check(logits, idx, top, weight)
+
+
+@pytest.mark.parametrize("mode", ["both", "lse"])
+def test_rows_without_a_finite_logit(mode):
+    logits, idx, top, weight = inputs(3, 500, 4, torch.float32, seed=10)
+    logits[1] = -math.inf
+    loss, lse, grad = nv.distill_topk_loss_and_grad(logits, idx, top, weight=weight)
+    if mode == "lse":
+        grad = nv.distill_topk_grad(logits, idx, top, lse, weight=weight)
+    assert lse[1].item() == -math.inf and loss[1].item() == math.inf
+    p = torch.softmax(top[1].double(), 0)
+    want = torch.zeros(500, dtype=torch.float64, device=DEV).scatter_add_(0, idx[1].long(), -p * weight[1].double())
+    assert ((grad[1].double() - want).abs() <= 64 * EPS * want.abs()).all()
+    ok = [0, 2]
+    check(logits[ok].contiguous(), idx[ok].contiguous(), top[ok].contiguous(), weight[ok].contiguous())
+
+
+def test_ignored_rows_hide_nan_and_others_show_it():
+    logits, idx, top, weight = inputs(4, 900, 4, torch.bfloat16, seed=11)
+    logits[:, 17] = math.nan
+    weight[1] = 0.0
+    idx[2] = -1
+    loss, lse, grad = nv.distill_topk_loss_and_grad(logits, idx, top, weight=weight)
+    alone = nv.distill_topk_grad(logits, idx, top, lse, weight=weight)
+    assert torch.isnan(lse).all()
+    for r, hidden in ((0, False), (1, True), (2, True), (3, False)):
+        if hidden:
+            assert loss[r].item() == 0 and not grad[r].any() and not alone[r].any()
+        else:
+            assert torch.isnan(loss[r]) and torch.isnan(grad[r]).all() and torch.isnan(alone[r]).all()
+
+
+@pytest.mark.parametrize("V,K", [(900, 40), (70000, 40)])
+def test_repeated_entries_add_up(V, K):
+    logits, idx, top, weight = inputs(5, V, K, torch.float32, seed=12)
+    idx[:, 10:] = idx[:, :10].repeat(1, 3)
+    check(logits, idx, top, weight)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V,pitch", [(1000, 1024), (1001, 1003), (33, 50)])
+def test_padded_rows(V, pitch, dtype):
+    logits, idx, top, weight = inputs(6, pitch, 8, dtype, seed=13)
+    idx %= V
+    for start in (0, 1, pitch - V):
+        check(logits[:, start:start + V], idx, top, weight)
+
+
+def test_no_rows():
+    logits, idx, top = (torch.empty(0, n, device=DEV) for n in (10, 3, 3))
+    loss, lse, grad = nv.distill_topk_loss_and_grad(logits, idx.int(), top)
+    assert loss.shape == (0,) and lse.shape == (0,) and grad.shape == (0, 10)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [5, 1001, 70001])
+def test_nothing_outside_the_gradient_is_written(V, dtype):
+    T = 3
+    logits, idx, top, weight = inputs(T, V, 3, dtype, seed=14)
+    buf = torch.full((T * V + 256,), 7.25, dtype=dtype, device=DEV)
+    loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    nv.nvfp4_distill_topk(logits, idx, top, weight, 1.0, loss, lse, buf[128:128 + T * V].view(T, V))
+    assert (buf[:128] == 7.25).all() and (buf[128 + T * V:] == 7.25).all()
+
+
+def test_gradient_against_differences():
+    """The kernel's gradient (float32) against central differences of the 64-bit loss."""
+    logits, idx, top, weight = inputs(2, 40, 6, torch.float32, seed=15, spread=1.0)
+    tau, e = 1.7, 1e-5
+    grad = nv.distill_topk_loss_and_grad(logits, idx, top, weight=weight, temperature=tau)[2]
+    for v in range(40):
+        step = torch.zeros(2, 40, dtype=torch.float64, device=DEV)
+        step[:, v] = e
+        up = definition(logits.double() + step, idx, top, weight, tau)[0]
+        down = definition(logits.double() - step, idx, top, weight, tau)[0]
+        assert (grad[:, v].double() - (up - down) / (2 * e)).abs().max().item() < 1e-6

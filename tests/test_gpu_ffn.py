@@ -1,0 +1,198 @@
+"""GPU checks of the gated feed-forward block against its definition in 64
+bits on the values the operands encode.
+
+Tolerance.  a pre-activation differs from the exact sum by at most
+d = (K / 16 + 4) 2^-24 sum|x w| (one rounding per 16-element block and the two
+tensor scales).  |act'| <= 1.13 for both activations, so h = act(a) u moves by
+at most 1.13 d_a |u| + |act(a)| d_u + 1.13 d_a d_u; its fp32 evaluation adds a
+relative error of the sigmoid's argument y (|y| 2^-23 through the exponential,
+with y itself good to four roundings) and a dozen roundings more.  The output's
+own rounding is half a step, 2^-8 (bf16) or 2^-24 of the value.  For the
+gradients |act''| <= 1.2 bounds how far act' moves with a."""
+import math
+
+import pytest
+import torch
+
+import bit_block_scaled_quant_amd as nv
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+E2M1 = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+
+
+def values(q):
+    """float64 values of an NVFP4 tensor (element 2k in the low nibble; E4M3 scales)."""
+    codes, scales = q.codes.long(), q.scales.long()
+    nib = torch.stack([codes & 15, codes >> 4], 2).flatten(1)
+    lut = torch.tensor(E2M1 + [-v for v in E2M1], dtype=torch.float64, device=codes.device)
+    e, man = scales >> 3, (scales & 7).double()
+    sc = torch.where(e == 0, man / 512, (1 + man / 8) * torch.exp2(e.double() - 7))
+    return lut[nib] * sc.repeat_interleave(16, 1) / q.tensor_scale[0].double()
+
+
+def operands(M, F, K, seed, gain=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = gain * torch.randn(M, K, generator=g, device=DEV)
+    x[:, K // 3] *= 20.0
+    w = torch.randn(2 * F, K, generator=g, device=DEV) / math.sqrt(K)
+    return x, w, g
+
+
+def definition(xv, wv, F, act):
+    a, u = (xv @ part.t().contiguous() for part in wv.split(F))
+    if act == nv.SILU:
+        y = a
+        s = torch.sigmoid(y)
+        slope = s + a * s * torch.sigmoid(-y)
+    else:
+        y = 2 * math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3)
+        s = torch.sigmoid(y)
+        slope = s + a * s * torch.sigmoid(-y) * 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * a ** 2)
+    absum = (xv.abs() @ wv.abs().t().contiguous()) * ((xv.shape[1] / 16 + 4) * 2.0 ** -24)
+    d_a, d_u = absum.split(F, 1)
+    return a, u, a * s, slope, y.abs(), d_a, d_u
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def check(got, want, bound, what):
+    bound = bound + half_step(got.dtype) * (want.abs() + bound) + 1e-30
+    excess = (got.double() - want).abs() - bound
+    assert torch.isfinite(got).all(), what
+    assert excess.max().item() <= 0, f"{what}: off by {excess.max().item()} at {divmod(excess.argmax().item(), got.shape[1])}"
+
+
+def run(M, F, K, act, dtype, seed=1, gain=1.0):
+    x, w, g = operands(M, F, K, seed, gain)
+    qx, qw = nv.quantize(x), nv.quantize(w)
+    dh = (torch.randn(M, F, generator=g, device=DEV) * 0.1).to(dtype)
+    a, u, h, slope, y, d_a, d_u = definition(values(qx), values(qw), F, act)
+    ev = (6 * y + 16) * 2.0 ** -23
+    check(nv.gated_ffn(qx, qw, act, dtype=dtype), h * u,
+          1.13 * d_a * u.abs() + h.abs() * d_u + 1.13 * d_a * d_u + ev * (h * u).abs(), "h")
+    amax = torch.full((1,), -1.0, device=DEV)
+    dgu = nv.gated_ffn_grad(dh, qx, qw, act, amax=amax)
+    d = dh.double()
+    # act' = s + (slope - s): both parts carry the evaluation error
+    ev_slope = ev * (slope.abs() + 1.2)
+    check(dgu[:, :F], d * u * slope,
+          d.abs() * (d_u * (slope.abs() + 1.2 * d_a) + u.abs() * (1.2 * d_a + ev_slope) + 2.0 ** -22 * (u * slope).abs()),
+          "da")
+    check(dgu[:, F:], d * h, d.abs() * (1.13 * d_a + ev * h.abs()) + 2.0 ** -22 * (d * h).abs(), "du")
+    assert amax.item() == dgu.float().abs().max().item()
+
+
+SHAPES = [(1, 16, 16), (1, 5120, 512), (2, 24, 48), (7, 40, 80), (16, 64, 64), (17, 33, 192), (33, 1000, 320),
+          (45, 256, 1024), (64, 128, 256), (65, 127, 448), (128, 96, 96), (129, 65, 704), (200, 512, 960),
+          (256, 128, 512), (300, 272, 2112), (515, 400, 576), (512, 384, 768), (1024, 256, 1280)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("act", [nv.SILU, nv.GELU])
+@pytest.mark.parametrize("M,F,K", SHAPES)
+def test_block_and_gradient(M, F, K, act, dtype):
+    run(M, F, K, act, dtype, seed=M + F)
+
+
+@pytest.mark.parametrize("act", [nv.SILU, nv.GELU])
+def test_many_tiles(act):  # more tiles than compute units, ragged on every side
+    run(2100, 2736, 832, act, torch.bfloat16)
+
+
+@pytest.mark.parametrize("act", [nv.SILU, nv.GELU])
+@pytest.mark.parametrize("M", [3, 100, 600])
+def test_large_pre_activations(act, M):  # the sigmoid at 0 and 1, cubes of large values
+    run(M, 320, 512, act, torch.float32, gain=300.0)
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_zero_input(M):
+    qx = nv.quantize(torch.zeros(M, 256, device=DEV))
+    qw = nv.quantize(torch.randn(96, 256, device=DEV))
+    assert not nv.gated_ffn(qx, qw, nv.SILU).any()
+    assert not nv.gated_ffn_grad(torch.ones(M, 48, device=DEV), qx, qw, nv.GELU).any()
+
+
+@pytest.mark.parametrize("M,F,K", [(40, 64, 512), (300, 200, 512), (512, 256, 512)])
+def test_unaligned_operands_and_outputs(M, F, K):
+    """Codes on 8-byte boundaries, scales on any byte, dh and outputs on any element."""
+    x, w, g = operands(M, F, K, 5)
+    qx, qw = nv.quantize(x), nv.quantize(w)
+    want = nv.gated_ffn(qx, qw, nv.SILU)
+    dh = torch.randn(M, F, generator=g, device=DEV).bfloat16()
+    want_grad = nv.gated_ffn_grad(dh, qx, qw, nv.SILU)
+
+    def moved(t, shift):
+        buf = torch.empty(t.numel() + 64, dtype=t.dtype, device=DEV)
+        return buf[shift:shift + t.numel()].view(t.shape).copy_(t)
+
+    for q in (qx, qw):
+        q.codes, q.scales = moved(q.codes, 8), moved(q.scales, 1)
+    a, u, h, slope, y, d_a, d_u = definition(values(qx), values(qw), F, nv.SILU)
+    for got, ref in ((nv.gated_ffn(qx, qw, nv.SILU, out=moved(want, 1)), want),
+                     (nv.gated_ffn_grad(moved(dh, 1), qx, qw, nv.SILU, out=moved(want_grad, 1)), want_grad)):
+        # the same sums in another order of K: both are within d of the exact ones
+        scale = 4 * (d_a.max() + d_u.max()) * (1 + max(u.abs().max(), h.abs().max())) * max(1.0, dh.abs().max().item())
+        assert ((got.double() - ref.double()).abs() <= scale + 2.0 ** -7 * ref.double().abs()).all()
+
+
+@pytest.mark.parametrize("M,F,K", [(45, 130, 512), (300, 200, 640), (512, 256, 512)])
+def test_nothing_outside_the_output_is_written(M, F, K):
+    x, w, g = operands(M, F, K, 9)
+    qx, qw = nv.quantize(x), nv.quantize(w)
+    for rows, cols, call in ((M, F, lambda o: nv.gated_ffn(qx, qw, nv.SILU, out=o)),
+                             (M, 2 * F, lambda o: nv.gated_ffn_grad(torch.ones(M, F, device=DEV), qx, qw, out=o))):
+        buf = torch.full((rows * cols + 2048,), 7.25, device=DEV)
+        call(buf[1024:1024 + rows * cols].view(rows, cols))
+        assert (buf[:1024] == 7.25).all() and (buf[1024 + rows * cols:] == 7.25).all()
+
+
+def test_derivative_against_differences():
+    """The definition's act' above against central differences of its act, in 64 bits."""
+    a = torch.linspace(-12, 12, 4001, dtype=torch.float64, device=DEV)
+    one = torch.ones(1, 1, dtype=torch.float64, device=DEV)
+    e = 1e-5
+    for act in (nv.SILU, nv.GELU):
+        f = lambda v: definition(v[:, None], torch.cat([one, one]), 1, act)
+        slope = f(a)[3][:, 0]
+        diff = (f(a + e)[2] - f(a - e)[2])[:, 0] / (2 * e)
+        assert (slope - diff).abs().max().item() < 1e-9
+
+
+@pytest.mark.parametrize("rounding,rht", [(nv.RNE, False), (nv.SR, False), (nv.SR, True)])
+@pytest.mark.parametrize("M,F,K", [(48, 24, 64), (256, 128, 512), (320, 200, 448)])
+def test_backward(M, F, K, rounding, rht):
+    """dx and dw are the products of the quantized gradient with W and X: each
+    within the GEMM's tolerance of the 64-bit product of what
+    quantize_cast_transpose makes of gated_ffn_grad's output, bit for bit."""
+    x, w, g = operands(M, F, K, 3)
+    qx, qxt = nv.quantize_cast_transpose(x, rht_t=rht, rht_seed=4)
+    qw = nv.quantize_2d(w)
+    dh = (torch.randn(M, F, generator=g, device=DEV) * 1e-3).bfloat16()
+    dx, dw = nv.gated_ffn_backward(dh, qx, qxt, qw, nv.GELU, rounding=rounding, seed=6, seed_t=7, rht_t=rht, rht_seed=4)
+    dgu = nv.gated_ffn_grad(dh, qx, qw, nv.GELU)
+    q, qt = nv.quantize_cast_transpose(dgu, rounding=rounding, seed=6, seed_t=7, rht_t=rht, rht_seed=4)
+    for got, a, b in ((dx, values(q), values(qw.transposed())), (dw, values(qt), values(qxt))):
+        absum = a.abs() @ b.abs().t().contiguous()
+        err = (got.double() - a @ b.t().contiguous()).abs()
+        assert (err <= (a.shape[1] / 16 + 4) * 2.0 ** -24 * absum).all()
+    got = nv.gated_ffn_backward(dh, qx, qxt, qw, nv.GELU, rounding=rounding, seed=6, seed_t=7, rht_t=rht, rht_seed=4,
+                                dtype=torch.bfloat16)
+    assert torch.equal(got[0], dx.bfloat16()) and torch.equal(got[1], dw.bfloat16())
+
+
+@pytest.mark.parametrize("rounding", [nv.RNE, nv.SR])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_cast_transpose_with_amax(dtype, rounding):
+    x = torch.randn(144, 272, device=DEV).to(dtype)
+    want = nv.quantize_cast_transpose(x, rounding=rounding, seed=2, seed_t=3, rht_t=False)
+    q, qt = nv._alloc(144, 272, DEV, False), nv._alloc(272, 144, DEV, False)
+    q.tensor_scale[1] = x.float().abs().max()
+    nv.nvfp4_quantize_cast_transpose_with_amax(x, rounding, 2, 3, q.codes, q.scales, q.tensor_scale, qt.codes,
+                                               qt.scales, qt.tensor_scale)
+    for got, ref in zip((q, qt), want):
+        assert torch.equal(got.codes, ref.codes) and torch.equal(got.scales, ref.scales)
+        assert torch.equal(got.tensor_scale, ref.tensor_scale)

@@ -1,0 +1,217 @@
+"""Refusals of the feed-forward, distillation and embedding calls: the Python
+marshallers check every tensor, and the C entry points check every argument on
+the host, before any HIP call (so none of this needs a GPU)."""
+import ctypes
+
+import pytest
+import torch
+
+import bit_block_scaled_quant_amd as nv
+
+U8, F32, BF16, I32 = torch.uint8, torch.float32, torch.bfloat16, torch.int32
+
+
+def z(*shape, dtype=U8):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def ffn_args(M=5, F=24, K=64):
+    return dict(x_codes=z(M, K // 2), x_scales=z(M, K // 16), x_tensor_scale=z(2, dtype=F32),
+                w_codes=z(2 * F, K // 2), w_scales=z(2 * F, K // 16), w_tensor_scale=z(2, dtype=F32), M=M, F=F, K=K,
+                act=nv.SILU)
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("x_codes", z(5, 31)), ("x_scales", z(5, 3)), ("w_codes", z(24, 32)), ("w_scales", z(48, 4, dtype=F32)),
+    ("x_tensor_scale", z(0, dtype=F32)), ("w_tensor_scale", z(2)), ("h", z(5, 23, dtype=BF16)),
+    ("h", z(5, 24, dtype=torch.float16)), ("h", z(24, 5, dtype=BF16).t()),
+])
+def test_ffn_rejects_bad_tensors(name, bad):
+    a = dict(ffn_args(), h=z(5, 24, dtype=BF16))
+    a[name] = bad
+    with pytest.raises(ValueError, match=name):
+        nv.nvfp4_gated_ffn(**a)
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("dh", z(5, 24, dtype=F32)), ("dh", z(5, 48, dtype=BF16)), ("dgu", z(5, 24, dtype=BF16)),
+    ("dgu_amax", z(1, dtype=I32)), ("dgu_amax", z(0, dtype=F32)), ("w_codes", z(48, 31)),
+])
+def test_ffn_grad_rejects_bad_tensors(name, bad):
+    a = dict(ffn_args(), dh=z(5, 24, dtype=BF16), dgu=z(5, 48, dtype=BF16))
+    a[name] = bad
+    with pytest.raises(ValueError, match=name):
+        nv.nvfp4_gated_ffn_grad(**a)
+
+
+def quantized(rows, cols, transposed=False):
+    q = nv.Quantized(z(rows, cols // 2), z(rows, cols // 16), z(2, dtype=F32))
+    if transposed:
+        q.codes_t, q.scales_t = z(cols, rows // 2), z(cols, rows // 16)
+    return q
+
+
+def test_ffn_wrappers_reject_mismatched_operands():
+    x, w = quantized(32, 64), quantized(48, 64, True)
+    with pytest.raises(ValueError, match="K mismatch"):
+        nv.gated_ffn(x, quantized(48, 32))
+    with pytest.raises(ValueError, match="as many gate"):
+        nv.gated_ffn(x, quantized(47, 64))
+    dh = z(32, 24, dtype=BF16)
+    with pytest.raises(ValueError, match="x_t"):
+        nv.gated_ffn_backward(dh, x, quantized(32, 64), w)
+    with pytest.raises(ValueError, match="transposed"):
+        nv.gated_ffn_backward(dh, x, quantized(64, 32), quantized(48, 64))
+    with pytest.raises(ValueError, match="M % 16"):
+        nv.gated_ffn_backward(z(40, 24, dtype=BF16), quantized(40, 64), quantized(64, 40), w)
+    for call in (lambda: nv.gated_ffn(x, w), lambda: nv.gated_ffn_grad(dh, x, w),
+                 lambda: nv.gated_ffn_backward(dh, x, quantized(64, 32), w)):
+        with pytest.raises(ValueError, match="GPU memory"):
+            call()
+
+
+def test_cast_transpose_with_amax_rejects_bad_tensors():
+    x = z(32, 64, dtype=BF16)
+    a = dict(codes=z(32, 32), scales=z(32, 4), tensor_scale=z(2, dtype=F32), codes_t=z(64, 16), scales_t=z(64, 2),
+             tensor_scale_t=z(2, dtype=F32))
+    for name, bad in (("codes_t", z(64, 15)), ("tensor_scale_t", z(1, dtype=F32)), ("scales", z(32, 3))):
+        with pytest.raises(ValueError, match=name):
+            nv.nvfp4_quantize_cast_transpose_with_amax(x, 0, 0, 1, **dict(a, **{name: bad}))
+    with pytest.raises(ValueError, match="required"):
+        nv.nvfp4_quantize_cast_transpose_with_amax(x, 0, 0, 1, **dict(a, codes_t=None, scales_t=None))
+    with pytest.raises(ValueError, match="GPU memory"):
+        nv.nvfp4_quantize_cast_transpose_with_amax(x, 0, 0, 1, **a)
+
+
+def distill_args(T=4, V=50, K=3):
+    return dict(logits=z(T, V, dtype=BF16), idx=z(T, K, dtype=I32), top=z(T, K, dtype=F32), weight=z(T, dtype=F32),
+                temperature=1.0, loss=z(T, dtype=F32), lse=z(T, dtype=F32), grad=z(T, V, dtype=BF16))
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("logits", z(4, 50, dtype=torch.float16)), ("logits", z(200, dtype=BF16)), ("logits", z(50, 4, dtype=BF16).t()),
+    ("logits", z(1, 50, dtype=BF16).expand(4, 50)),
+    ("idx", z(4, 3, dtype=torch.int64)), ("idx", z(3, 3, dtype=I32)), ("idx", z(12, dtype=I32)),
+    ("top", z(4, 2, dtype=F32)), ("top", z(4, 3, dtype=BF16)), ("weight", z(3, dtype=F32)),
+    ("loss", z(5, dtype=F32)), ("lse", None), ("lse", z(4, dtype=BF16)), ("grad", z(4, 50, dtype=F32)),
+    ("grad", z(4, 64, dtype=BF16)[:, :50]),
+])
+def test_distill_rejects_bad_tensors(name, bad):
+    with pytest.raises(ValueError, match=name):
+        nv.nvfp4_distill_topk(**dict(distill_args(), **{name: bad}))
+
+
+def test_distill_accepts_padded_rows_up_to_the_gpu_check():
+    with pytest.raises(ValueError, match="GPU memory"):
+        nv.nvfp4_distill_topk(**dict(distill_args(), logits=z(4, 64, dtype=BF16)[:, :50]))
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("tokens", z(4, dtype=torch.int64)), ("tokens", z(2, 2, dtype=I32)), ("table", z(8, 6, dtype=torch.float16)),
+    ("table", z(48, dtype=BF16)), ("out", z(4, 5, dtype=BF16)), ("out", z(4, 6, dtype=F32)),
+    ("table", z(6, 8, dtype=BF16).t()),
+])
+def test_embed_rejects_bad_tensors(name, bad):
+    a = dict(tokens=z(4, dtype=I32), table=z(8, 6, dtype=BF16), scale=1.0, out=z(4, 6, dtype=BF16))
+    with pytest.raises(ValueError, match=name):
+        nv.nvfp4_embed(**dict(a, **{name: bad}))
+    with pytest.raises(ValueError, match="GPU memory"):
+        nv.nvfp4_embed(**a)
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("tokens", z(5, dtype=I32)), ("tokens", z(4, dtype=torch.int64)), ("dout", z(4, 6, dtype=torch.float64)),
+    ("grad", z(8, 5, dtype=F32)), ("grad", z(8, 6, dtype=BF16)), ("grad", z(48, dtype=F32)),
+])
+def test_embed_grad_rejects_bad_tensors(name, bad):
+    a = dict(tokens=z(4, dtype=I32), dout=z(4, 6, dtype=BF16), scale=1.0, grad=z(8, 6, dtype=F32))
+    with pytest.raises(ValueError, match=name):
+        nv.nvfp4_embed_grad(**dict(a, **{name: bad}))
+    with pytest.raises(ValueError, match="GPU memory"):
+        nv.nvfp4_embed_grad(**a)
+
+
+# ---- the C entry points (fake, well-aligned device addresses) -----------------
+A = ctypes.c_void_p(0x10000)
+
+
+def off(n):
+    return ctypes.c_void_p(0x10000 + n)
+
+
+def c_ffn(x=A, xs=A, xt=A, w=A, ws=A, wt=A, M=16, F=16, K=32, act=0, out=A, dtype=1):
+    return nv.lib().nvfp4_gated_ffn(x, xs, xt, w, ws, wt, M, F, K, act, out, dtype, None)
+
+
+def c_ffn_grad(x=A, xs=A, xt=A, w=A, ws=A, wt=A, M=16, F=16, K=32, act=0, dh=A, out=A, dtype=1, amax=None):
+    return nv.lib().nvfp4_gated_ffn_grad(x, xs, xt, w, ws, wt, M, F, K, act, dh, out, dtype, amax, None)
+
+
+@pytest.mark.parametrize("call", [c_ffn, c_ffn_grad])
+@pytest.mark.parametrize("kw,status", [
+    (dict(x=None), -1), (dict(ws=None), -1), (dict(wt=None), -1), (dict(out=None), -1), (dict(act=2), -1),
+    (dict(act=-1), -1), (dict(dtype=2), -1), (dict(M=0), -2), (dict(F=0), -2), (dict(K=0), -2), (dict(K=24), -2),
+    (dict(M=65535 * 128 + 1), -2), (dict(F=(1 << 30) + 1), -2), (dict(F=1 << 20, K=1 << 20), -2),
+    (dict(M=1 << 20, F=1 << 20), -2), (dict(M=1 << 21, K=1 << 20), -2), (dict(x=off(4)), -3), (dict(w=off(4)), -3),
+    (dict(xt=off(2)), -3), (dict(out=off(1)), -3), (dict(out=off(2), dtype=0), -3),
+])
+def test_c_gated_ffn_rejects(call, kw, status):
+    assert call(**kw) == status
+
+
+def test_c_gated_ffn_grad_rejects():
+    assert c_ffn_grad(dh=None) == -1
+    assert c_ffn_grad(dh=off(1)) == -3
+    assert c_ffn_grad(amax=off(2)) == -3
+
+
+def test_c_cast_transpose_with_amax_rejects():
+    def ct(x=A, dtype=1, rows=32, cols=64, rounding=0, codes=A, scales=A, ts=A, codes_t=A, scales_t=A, ts_t=A):
+        return nv.lib().nvfp4_quantize_cast_transpose_with_amax(x, dtype, rows, cols, rounding, 0, 1, codes, scales,
+                                                                ts, codes_t, scales_t, ts_t, None)
+    assert ct(codes_t=None) == -1 and ct(scales_t=None) == -1 and ct(ts_t=None) == -1 and ct(x=None) == -1
+    assert ct(dtype=3) == -1 and ct(rounding=2) == -1
+    assert ct(rows=40) == -2 and ct(cols=40) == -2 and ct(rows=0) == -2
+    assert ct(x=off(8)) == -3 and ct(ts_t=off(2)) == -3 and ct(codes_t=off(4)) == -3
+
+
+def c_distill(logits=A, dtype=1, T=4, V=50, stride=50, idx=A, top=A, K=3, weight=A, tau=1.0, loss=A, lse=A, grad=A):
+    return nv.lib().nvfp4_distill_topk(logits, dtype, T, V, stride, idx, top, K, weight, ctypes.c_float(tau), loss,
+                                       lse, grad, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(logits=None), -1), (dict(idx=None), -1), (dict(top=None), -1), (dict(lse=None), -1),
+    (dict(loss=None, grad=None), -1), (dict(dtype=2), -1), (dict(tau=0.0), -1), (dict(tau=-1.0), -1),
+    (dict(tau=float("nan")), -1), (dict(tau=float("inf")), -1),
+    (dict(T=-1), -2), (dict(T=1 << 22), -2), (dict(V=0), -2), (dict(V=1 << 31, stride=1 << 31), -2),
+    (dict(stride=49), -2), (dict(stride=1 << 39), -2), (dict(K=0), -2), (dict(K=1025), -2),
+    (dict(logits=off(1)), -3), (dict(logits=off(2), dtype=0), -3), (dict(idx=off(2)), -3), (dict(top=off(2)), -3),
+    (dict(weight=off(2)), -3), (dict(loss=off(2)), -3), (dict(lse=off(2)), -3), (dict(grad=off(1)), -3),
+])
+def test_c_distill_rejects(kw, status):
+    assert c_distill(**kw) == status
+
+
+def test_c_empty_calls_enqueue_nothing():
+    assert c_distill(T=0, logits=None, idx=None, top=None, weight=None, loss=None, lse=None, grad=None) == 0
+    assert nv.lib().nvfp4_embed(None, 0, A, 1, 8, 6, ctypes.c_float(1.0), None, None) == 0
+
+
+def c_embed(tok=A, T=4, table=A, dtype=1, V=8, D=6, scale=1.0, out=A):
+    return nv.lib().nvfp4_embed(tok, T, table, dtype, V, D, ctypes.c_float(scale), out, None)
+
+
+def c_embed_grad(tok=A, T=4, table=A, dtype=1, V=8, D=6, scale=1.0, out=A):
+    return nv.lib().nvfp4_embed_grad(tok, T, table, dtype, V, D, ctypes.c_float(scale), out, None)
+
+
+@pytest.mark.parametrize("call", [c_embed, c_embed_grad])
+@pytest.mark.parametrize("kw,status", [
+    (dict(tok=None), -1), (dict(table=None), -1), (dict(out=None), -1), (dict(dtype=2), -1),
+    (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(T=-1), -2), (dict(V=0), -2),
+    (dict(V=(1 << 27) + 1), -2), (dict(D=0), -2), (dict(V=1 << 27, D=1 << 14), -2), (dict(T=1 << 35, D=1 << 6), -2),
+    (dict(tok=off(2)), -3), (dict(table=off(1)), -3), (dict(table=off(2), dtype=0), -3), (dict(out=off(1)), -3),
+])
+def test_c_embed_rejects(call, kw, status):
+    assert call(**kw) == status
