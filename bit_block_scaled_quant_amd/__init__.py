@@ -92,7 +92,9 @@ def lib():
         L.nvfp4_embed.restype = I
         L.nvfp4_embed.argtypes = [P, I64, P, I, I64, I64, F, P, P]
         L.nvfp4_embed_grad.restype = I
-        L.nvfp4_embed_grad.argtypes = [P, I64, P, I, I64, I64, F, P, P]
+        L.nvfp4_embed_grad.argtypes = [P, I64, P, I, I64, I64, F, P, P, P]
+        L.nvfp4_embed_grad_workspace.restype = I64
+        L.nvfp4_embed_grad_workspace.argtypes = [I64]
         L.nvfp4_status_string.restype = ctypes.c_char_p
         L.nvfp4_status_string.argtypes = [I]
         L.nvfp4_last_error.restype = ctypes.c_char_p
@@ -367,15 +369,21 @@ def nvfp4_embed(tokens, table, scale, out):
                              _stream(table)), "nvfp4_embed")
 
 
-def nvfp4_embed_grad(tokens, dout, scale, grad):
+def nvfp4_embed_grad_workspace(tokens):
+    """Bytes of scratch memory that nvfp4_embed_grad takes for so many tokens."""
+    return lib().nvfp4_embed_grad_workspace(int(tokens))
+
+
+def nvfp4_embed_grad(tokens, dout, scale, grad, workspace):
     T, D, dev = _want_input(dout, "dout")
     if _want_tokens(tokens, dev) != T:
         raise ValueError(f"nvfp4: tokens must have {T} elements, got {tokens.shape[0]}")
     if not isinstance(grad, torch.Tensor) or grad.dim() != 2:
         raise ValueError("nvfp4: grad must be a 2-D tensor")
     _want(grad, "grad", _F32, dev, (grad.shape[0], D))
+    _want(workspace, "workspace", _U8, dev, min_numel=nvfp4_embed_grad_workspace(T))
     _check(lib().nvfp4_embed_grad(_ptr(tokens), T, _ptr(dout), _dtype(dout), grad.shape[0], D, float(scale),
-                                  _ptr(grad), _stream(dout)), "nvfp4_embed_grad")
+                                  _ptr(grad), _ptr(workspace), _stream(dout)), "nvfp4_embed_grad")
 
 
 # ---- convenience wrappers ---------------------------------------------------
@@ -604,5 +612,6 @@ def embed(tokens, table, scale=1.0):
 def embed_grad(tokens, dout, rows, scale=1.0):
     """The fp32 gradient [rows][D] of embed's table for the gradient dout [T][D]."""
     grad = torch.empty(rows, dout.shape[1], dtype=torch.float32, device=dout.device)
-    nvfp4_embed_grad(tokens, dout, scale, grad)
+    space = torch.empty(nvfp4_embed_grad_workspace(tokens.shape[0]), dtype=torch.uint8, device=dout.device)
+    nvfp4_embed_grad(tokens, dout, scale, grad, space)
     return grad

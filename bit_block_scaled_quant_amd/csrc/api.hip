@@ -353,24 +353,31 @@ int nvfp4_embed(const int32_t* tokens, int64_t T, const void* table, int dtype, 
   int cus = 0;
   int st = device_cus(&cus);
   if (st) return st;
-  nvfp4::EmbedArgs a{tokens, T, V, D, dtype == NVFP4_BF16, scale, table, out};
+  nvfp4::EmbedArgs a{tokens, T, V, D, dtype == NVFP4_BF16, scale, table, out, nullptr, nullptr, nullptr};
   nvfp4::launch_embed(a, cus, (hipStream_t)stream);
   return check_launch("nvfp4_embed");
 }
 
+int64_t nvfp4_embed_grad_workspace(int64_t T) {
+  return T < 0 || T >= nvfp4::kEmbedMaxTokens ? 0 : nvfp4::embed_grad_workspace(T);
+}
+
 int nvfp4_embed_grad(const int32_t* tokens, int64_t T, const void* dout, int dtype, int64_t V, int64_t D,
-                     float scale, float* grad, void* stream) {
-  if (!grad || (T != 0 && (!tokens || !dout))) return NVFP4_ERR_ARG;
+                     float scale, float* grad, void* workspace, void* stream) {
+  if (!grad || (T != 0 && (!tokens || !dout || !workspace))) return NVFP4_ERR_ARG;
   if (dtype != NVFP4_F32 && dtype != NVFP4_BF16) return NVFP4_ERR_ARG;
   if (!std::isfinite(scale)) return NVFP4_ERR_ARG;
-  if (T < 0 || V <= 0 || V > (INT64_C(1) << 27) || D <= 0 || !size_ok(V, D) || !size_ok(T, D))
+  if (T < 0 || T >= nvfp4::kEmbedMaxTokens || V <= 0 || V > (INT64_C(1) << 27) || D <= 0 ||
+      D > (INT64_C(1) << 18) || V * D > (INT64_C(1) << 33))  // a lane per 4 elements, a 32-bit grid
     return NVFP4_ERR_SHAPE;
-  if (!aligned(tokens, 4) || !aligned(dout, dtype == NVFP4_F32 ? 4 : 2) || !aligned(grad, 4)) return NVFP4_ERR_ALIGN;
+  if (!aligned(tokens, 4) || !aligned(dout, dtype == NVFP4_F32 ? 4 : 2) || !aligned(grad, 4) ||
+      !aligned(workspace, 8))
+    return NVFP4_ERR_ALIGN;
   int cus = 0;
   int st = device_cus(&cus);
   if (st) return st;
-  nvfp4::EmbedArgs a{tokens, T, V, D, dtype == NVFP4_BF16, scale, dout, grad};
-  nvfp4::launch_embed_grad(a, cus, (hipStream_t)stream);
+  nvfp4::EmbedArgs a{tokens, T, V, D, dtype == NVFP4_BF16, scale, dout, grad, nullptr, nullptr, nullptr};
+  nvfp4::launch_embed_grad(a, workspace, cus, (hipStream_t)stream);
   return check_launch("nvfp4_embed_grad");
 }
 

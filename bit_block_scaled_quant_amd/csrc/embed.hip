@@ -53,184 +53,304 @@ __global__ __launch_bounds__(kEmbThreads) void k_embed(EmbedArgs p, int lpr_log2
 }
 
 // ---- gradient of the table ------------------------------------------------
-// A workgroup owns up to 64 consecutive rows of the table and a chunk of
-// columns, four columns a lane.  It reads all tokens (they stay in L2) and
-// lists those of its rows in the order of their positions, so nothing is
-// sorted, counted or scattered beforehand, no two workgroups write one row,
-// and every sum has one order.  Rows without tokens are written as zeros.
+// 1. k_embed_sort: each workgroup sorts 8192 tokens by row, stably, in LDS.
+//    Past 8192 tokens, k_embed_merge merges pairs of sorted runs, each entry
+//    finding its place by a binary search, once for each doubling.
+// 2. k_embed_fill writes zeros everywhere, which bounds a training batch (2.7
+//    GB for [131072][5120]).  The store must wait for nothing and be the only
+//    one of its thread: 390 us for one 16-byte store a thread in workgroups of
+//    256, 435 for two, 470 for eight, 550 for a grid-stride loop, and 555 when
+//    each thread also looks up whether its row has tokens (measured; with that
+//    the rows below would not be written twice, 3% of the bytes).
+// 3. k_embed_few: the lanes at an entry that begins a row sum the row if it has
+//    at most kFew entries, and list it otherwise.
+// 4. k_embed_many sums the listed rows, a workgroup per 256 columns.
+// Every sum has one order: that of the positions, cut into equal parts for the
+// groups that share a row.
 //
-// Tokens are taken kBatch at a time, each wave listing a quarter.  The rows a
-// batch names are numbered (their rank in a 64-bit mask) and summed kSlots at
-// a time in LDS: group g of 2^lpr_log2 lanes adds every G-th entry to its own
-// copy, then the copies are joined in the order of the groups.  A row named
-// in a later batch again is read, added to and written.
-constexpr int kBatch = 4096, kWaveBatch = kBatch / 4;
-constexpr int kSlots = 4;
-constexpr int kAhead = 8;  // rows of dout in flight per lane
+// One launch in which every workgroup owned 64 rows, read all tokens and
+// listed its own took 538 us for 8192 tokens of [131072][5120], since a CU's
+// few workgroups listed, summed and wrote in turn.
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kRun = 8192, kPer = kRun / kSortThreads;  // entries a run, at most a thread
+constexpr int kFew = 8;
+constexpr int kManyThreads = 1024;
+
+// four columns of a row, as loaded
+template <bool BF16>
+struct Four {
+  uint32_t w[BF16 ? 2 : 4];
+  __device__ __forceinline__ float operator[](int k) const {
+    if (!BF16) return __uint_as_float(w[k % (BF16 ? 2 : 4)]);
+    return __uint_as_float((k & 1) ? (w[k >> 1] & 0xFFFF0000u) : (w[k >> 1] << 16));
+  }
+};
 
 template <bool BF16>
-__device__ __forceinline__ void load4(const EmbedArgs& p, int64_t t, int64_t col, float (&x)[4]) {
+__device__ __forceinline__ Four<BF16> load4(const EmbedArgs& p, int64_t t, int64_t col) {
   const int64_t i = t * p.D + col;
+  Four<BF16> x;
   if (col + 4 <= p.D) {
     if (BF16) {
       const u32x2_a2 w = *reinterpret_cast<const u32x2_a2*>(static_cast<const uint16_t*>(p.in) + i);
-      x[0] = __uint_as_float(w[0] << 16);
-      x[1] = __uint_as_float(w[0] & 0xFFFF0000u);
-      x[2] = __uint_as_float(w[1] << 16);
-      x[3] = __uint_as_float(w[1] & 0xFFFF0000u);
+      x.w[0] = w[0];
+      x.w[1] = w[1];
     } else {
-      const f32x4_a4 w = *reinterpret_cast<const f32x4_a4*>(static_cast<const float*>(p.in) + i);
+      const u32x4_a2 w = *reinterpret_cast<const u32x4_a2*>(static_cast<const float*>(p.in) + i);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = w[k];
+      for (int k = 0; k < (BF16 ? 2 : 4); ++k) x.w[k] = w[k];
     }
   } else {
 #pragma unroll
+    for (int k = 0; k < (BF16 ? 2 : 4); ++k) x.w[k] = 0u;
+#pragma unroll
     for (int k = 0; k < 4; ++k) {
-      x[k] = 0.0f;
-      if (col + k < p.D)
-        x[k] = BF16 ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(p.in)[i + k] << 16)
-                    : static_cast<const float*>(p.in)[i + k];
+      if (col + k >= p.D) continue;
+      if (BF16)
+        x.w[k >> 1] |= (uint32_t) static_cast<const uint16_t*>(p.in)[i + k] << (16 * (k & 1));
+      else
+        x.w[k % (BF16 ? 2 : 4)] = static_cast<const uint32_t*>(p.in)[i + k];
     }
   }
+  return x;
 }
 
-template <bool ADD>
 __device__ __forceinline__ void store4(const EmbedArgs& p, int64_t row, int64_t col, f32x4_a4 v) {
   float* dst = static_cast<float*>(p.out) + row * p.D + col;
   if (col + 4 <= p.D) {
-    if (ADD) v += *reinterpret_cast<const f32x4_a4*>(dst);
     *reinterpret_cast<f32x4_a4*>(dst) = v;
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (col + k < p.D) dst[k] = ADD ? dst[k] + v[k] : v[k];
+      if (col + k < p.D) dst[k] = v[k];
   }
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(kEmbThreads) void k_embed_grad(EmbedArgs p, int lpr_log2, int rows_per, int64_t chunks) {
-  __shared__ uint32_t s_list[4][kWaveBatch];  // position in the batch << 6 | row of the workgroup
-  __shared__ int s_count[4];
-  __shared__ unsigned long long s_mask;
-  __shared__ float s_acc[kSlots * kEmbThreads * 4];  // [slot][thread][4]
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int lpr = 1 << lpr_log2, group = tid >> lpr_log2, groups = kEmbThreads >> lpr_log2;
-  const int64_t v0 = (int64_t)(blockIdx.x / chunks) * rows_per;
-  const int64_t col = ((int64_t)(blockIdx.x % chunks) * lpr + (tid & (lpr - 1))) * 4;
-  const int n = (int)min<int64_t>(rows_per, p.V - v0);
-  unsigned long long done = 0;  // rows written so far
+// the lanes of the wave whose low six bits of `key` are this lane's
+__device__ __forceinline__ unsigned long long same_key(uint32_t key) {
+  unsigned long long same = ~0ull;
+#pragma unroll
+  for (int b = 0; b < 6; ++b) {
+    const unsigned long long set = __ballot((key >> b) & 1u);
+    same &= ((key >> b) & 1u) ? set : ~set;
+  }
+  return same;
+}
 
-  for (int64_t t0 = 0; t0 < p.T; t0 += kBatch) {
-    if (tid == 0) s_mask = 0;
+// A least-significant-digit radix sort of one run, six bits a pass.  Wave w
+// holds the w-th part of the present order, 64 entries at a time: an entry's
+// rank among its wave's equal digits is the count before plus the equal lanes
+// below.  Tokens outside the table and the entries past T take key V, the
+// largest.
+__global__ __launch_bounds__(kSortThreads) void k_embed_sort(EmbedArgs p, int bits) {
+  __shared__ uint32_t s_key[kRun];
+  __shared__ uint16_t s_pos[kRun];
+  __shared__ int s_at[kSortWaves][64];  // a wave's entries of each digit, then where they go
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t t0 = (int64_t)blockIdx.x * kRun;
+  // a lone run needs no more rounds than its tokens fill; others are merged whole
+  const int per = gridDim.x > 1 ? kPer : (int)((p.T + kSortThreads - 1) / kSortThreads);
+  const int mine = wave * 64 * per + lane;
+  uint32_t key[kPer];
+  int pos[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (k >= per) break;
+    pos[k] = mine + 64 * k;
+    const int64_t t = t0 + pos[k];
+    const uint32_t tok = t < p.T ? (uint32_t)p.tok[t] : ~0u;
+    key[k] = tok < (uint32_t)p.V ? tok : (uint32_t)p.V;
+  }
+  if (blockIdx.x == 0 && tid == 0) *p.count = 0u;
+  for (int shift = 0; shift < bits; shift += 6) {
+    s_at[wave][lane] = 0;
+    __builtin_amdgcn_wave_barrier();
+    int rank[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (k >= per) break;
+      const uint32_t d = (key[k] >> shift) & 63u;
+      const unsigned long long same = same_key(d);
+      const int before = s_at[wave][d];
+      __builtin_amdgcn_wave_barrier();
+      rank[k] = before + __popcll(same & ((1ull << lane) - 1ull));
+      if ((same >> lane) == 1ull) s_at[wave][d] = before + __popcll(same);  // the last of the equal lanes
+      __builtin_amdgcn_wave_barrier();
+    }
     __syncthreads();
-    int count = 0;
-    unsigned long long mask = 0;
-    for (int i = 0; i < kWaveBatch; i += 256) {  // four tokens a lane
-      const int64_t t = t0 + wave * kWaveBatch + i + 4 * lane;
-      i32x4_a4 tk = {-1, -1, -1, -1};
-      if (t + 4 <= p.T) {
-        tk = *reinterpret_cast<const i32x4_a4*>(p.tok + t);
-      } else {
+    if (wave == 0) {
+      int count[kSortWaves], all = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (t + k < p.T) tk[k] = p.tok[t + k];
-      }
-      int found = 0;
-      uint32_t r[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t d = (int64_t)tk[k] - v0;
-        const bool in = d >= 0 && d < n;
-        r[k] = in ? (uint32_t)d : 64u;
-        found += in;
-      }
-      if (__ballot(found > 0) == 0) continue;  // wave-uniform
-      int before = found;  // inclusive prefix sum over the lanes
+      for (int w = 0; w < kSortWaves; ++w) all += count[w] = s_at[w][lane];
+      int sum = all;  // inclusive prefix sum over the digits
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
-        const int o = __shfl_up(before, off);
-        if (lane >= off) before += o;
+        const int o = __shfl_up(sum, off);
+        if (lane >= off) sum += o;
       }
-      const int all = __shfl(before, 63);
-      int at = count + before - found;
+      int base = sum - all;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (r[k] < 64u) {
-          s_list[wave][at++] = (uint32_t)(wave * kWaveBatch + i + 4 * lane + k) << 6 | r[k];
-          mask |= 1ull << r[k];
-        }
+      for (int w = 0; w < kSortWaves; ++w) {
+        s_at[w][lane] = base;
+        base += count[w];
       }
-      count += all;
     }
-    if (lane == 0) s_count[wave] = count;
-    if (mask) atomicOr(&s_mask, mask);
     __syncthreads();
-    const unsigned long long named = s_mask;
-    const int c0 = s_count[0], c1 = c0 + s_count[1], c2 = c1 + s_count[2], total = c2 + s_count[3];
-    const int nrows = __popcll(named);
-    for (int s0 = 0; s0 < nrows; s0 += kSlots) {
 #pragma unroll
-      for (int s = 0; s < kSlots; ++s) {
-        f32x4_a4 zero = {0.f, 0.f, 0.f, 0.f};
-        *reinterpret_cast<f32x4_a4*>(s_acc + (s * kEmbThreads + tid) * 4) = zero;
-      }
-      if (col < p.D) {
-        for (int e0 = group; e0 < total; e0 += kAhead * groups) {
-          float x[kAhead][4];
-          int slot[kAhead];
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            const int e = e0 + k * groups;
-            slot[k] = kSlots;
-            if (e < total) {
-              const int w = (e >= c0) + (e >= c1) + (e >= c2);
-              const uint32_t it = s_list[w][e - (w == 0 ? 0 : w == 1 ? c0 : w == 2 ? c1 : c2)];
-              const int rank = __popcll(named & ((1ull << (it & 63u)) - 1ull)) - s0;
-              if (rank >= 0 && rank < kSlots) {
-                slot[k] = rank;
-                load4<BF16>(p, t0 + (it >> 6), col, x[k]);
-              }
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            if (slot[k] < kSlots) {
-              float* a = s_acc + (slot[k] * kEmbThreads + tid) * 4;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) a[j] += x[k][j];
-            }
-          }
-        }
-      }
-      __syncthreads();
-      // join: group g takes slots g, g + groups, ..
-      for (int s = group; s < kSlots && s0 + s < nrows; s += groups) {
-        unsigned long long m = named;
-        for (int i = 0; i < s0 + s; ++i) m &= m - 1;
-        const int r = __ffsll(m) - 1;
-        f32x4_a4 sum = {0.f, 0.f, 0.f, 0.f};
-        for (int g = 0; g < groups; ++g) {
-          const float* a = s_acc + (s * kEmbThreads + (g << lpr_log2) + (tid & (lpr - 1))) * 4;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sum[j] += a[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum[j] *= p.scale;
-        if (col < p.D) {
-          if (done >> r & 1)
-            store4<true>(p, v0 + r, col, sum);
-          else
-            store4<false>(p, v0 + r, col, sum);
-        }
-      }
-      __syncthreads();
+    for (int k = 0; k < kPer; ++k) {
+      if (k >= per) break;
+      const int to = s_at[wave][(key[k] >> shift) & 63u] + rank[k];
+      s_key[to] = key[k];
+      s_pos[to] = (uint16_t)pos[k];
     }
-    done |= named;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (k >= per) break;
+      key[k] = s_key[mine + 64 * k];
+      pos[k] = s_pos[mine + 64 * k];
+    }
   }
-  const f32x4_a4 zero = {0.f, 0.f, 0.f, 0.f};
-  if (col < p.D)
-    for (int r = group; r < n; r += groups)
-      if (!(done >> r & 1)) store4<false>(p, v0 + r, col, zero);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (k >= per) break;
+    const int at = mine + 64 * k;
+    p.sorted[t0 + at] = make_uint2(key[k], (uint32_t)(t0 + pos[k]));
+  }
+}
+
+// Runs of `len` sorted entries of src, merged in pairs into dst: an entry of
+// the left run goes past the smaller ones of the right, one of the right run
+// past the smaller and equal ones of the left.
+__global__ __launch_bounds__(kEmbThreads) void k_embed_merge(const uint2* __restrict__ src, uint2* __restrict__ dst,
+                                                             int64_t n, int64_t len) {
+  const int64_t i = (int64_t)blockIdx.x * kEmbThreads + threadIdx.x;
+  if (i >= n) return;
+  const int64_t pair = i / (2 * len) * (2 * len), mid = min(pair + len, n), end = min(pair + 2 * len, n);
+  const uint2 e = src[i];
+  const bool left = i < mid;
+  const int64_t other = left ? mid : pair;
+  int64_t lo = other, hi = left ? end : mid;
+  while (lo < hi) {
+    const int64_t m = (lo + hi) / 2;
+    if (src[m].x < e.x || (!left && src[m].x == e.x))
+      lo = m + 1;
+    else
+      hi = m;
+  }
+  dst[i + (lo - other) - (left ? 0 : mid - pair)] = e;
+}
+
+__global__ __launch_bounds__(kEmbThreads) void k_embed_fill(float* out, int64_t n) {
+  const int64_t i = ((int64_t)blockIdx.x * kEmbThreads + threadIdx.x) * 4;
+  if (i + 4 <= n) {
+    *reinterpret_cast<f32x4_a4*>(out + i) = f32x4_a4{0.f, 0.f, 0.f, 0.f};
+  } else {
+    for (int64_t e = i; e < n; ++e) out[e] = 0.0f;
+  }
+}
+
+// 2^lpr_log2 lanes an entry, kWide vectors of four columns a lane, two entries
+// of the row in flight
+template <bool BF16>
+__global__ __launch_bounds__(kEmbThreads) void k_embed_few(EmbedArgs p, int lpr_log2) {
+  constexpr int kWide = 4;
+  const int lpr = 1 << lpr_log2, l = threadIdx.x & (lpr - 1);
+  const int64_t i = ((int64_t)blockIdx.x * kEmbThreads + threadIdx.x) >> lpr_log2;
+  if (i >= p.T) return;
+  // entries i - 1 .. i + kFew, all at once
+  const uint32_t before = i > 0 ? p.sorted[i - 1].x : ~0u;
+  uint2 e[kFew + 1];
+#pragma unroll
+  for (int k = 0; k <= kFew; ++k) e[k] = i + k < p.T ? p.sorted[i + k] : make_uint2(~0u, 0u);
+  const uint32_t row = e[0].x;
+  if (row >= p.V || before == row) return;
+  if (e[kFew].x == row) {
+    if (l == 0 && blockIdx.y == 0) {  // the row's end, by bisection
+      int64_t lo = i + kFew + 1, hi = p.T;
+      while (lo < hi) {
+        const int64_t m = (lo + hi) / 2;
+        if (p.sorted[m].x == row)
+          lo = m + 1;
+        else
+          hi = m;
+      }
+      p.many[atomicAdd(p.count, 1u)] = make_uint2((uint32_t)i, (uint32_t)(lo - i));  // (any order will do)
+    }
+    return;
+  }
+  const int64_t c0 = (int64_t)blockIdx.y * 4 * kWide * lpr + 4 * l;
+  float acc[kWide][4] = {};
+#pragma unroll
+  for (int q = 0; q < kFew; q += 2) {
+    if (e[q].x != row) break;
+    const bool two = e[q + 1].x == row;
+    Four<BF16> x[kWide], y[kWide];
+#pragma unroll
+    for (int w = 0; w < kWide; ++w) {
+      const int64_t col = c0 + 4 * w * lpr;
+      if (col < p.D) x[w] = load4<BF16>(p, e[q].y, col);
+      if (col < p.D && two) y[w] = load4<BF16>(p, e[q + 1].y, col);
+    }
+#pragma unroll
+    for (int w = 0; w < kWide; ++w) {
+      if (c0 + 4 * w * lpr >= p.D) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[w][j] += x[w][j];
+      if (!two) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[w][j] += y[w][j];
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < kWide; ++w) {
+    const int64_t col = c0 + 4 * w * lpr;
+    if (col < p.D)
+      store4(p, row, col, f32x4_a4{acc[w][0] * p.scale, acc[w][1] * p.scale, acc[w][2] * p.scale, acc[w][3] * p.scale});
+  }
+}
+
+// One listed row and 4 * 2^lpr_log2 columns a workgroup at a time: each group
+// of lanes sums its part of the row's entries, the first joins the parts.
+template <bool BF16>
+__global__ __launch_bounds__(kManyThreads) void k_embed_many(EmbedArgs p, int lpr_log2, uint32_t chunks) {
+  constexpr int kAhead = 8;  // rows of dout in flight per lane
+  __shared__ __align__(16) float s_sum[kManyThreads * 4];
+  const int tid = threadIdx.x, lpr = 1 << lpr_log2;
+  const int group = tid >> lpr_log2, groups = kManyThreads >> lpr_log2;
+  const uint64_t tasks = (uint64_t)*p.count * chunks;
+  for (uint64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const uint2 listed = p.many[task / chunks];
+    const int64_t i = listed.x, n = listed.y;
+    const int64_t col = ((int64_t)(task % chunks) * lpr + (tid & (lpr - 1))) * 4;
+    const bool on = col < p.D;
+    const int64_t part = (n + groups - 1) / groups, q0 = i + group * part, q1 = min(q0 + part, i + n);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    if (on) {
+      for (int64_t q = q0; q < q1; q += kAhead) {
+        Four<BF16> x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (q + k < q1) x[k] = load4<BF16>(p, p.sorted[q + k].y, col);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          if (q + k >= q1) break;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] += x[k][j];
+        }
+      }
+    }
+    *reinterpret_cast<f32x4_a4*>(s_sum + 4 * tid) = f32x4_a4{acc[0], acc[1], acc[2], acc[3]};
+    __syncthreads();
+    if (group == 0 && on) {
+      for (int g = 1; g < groups && g * part < n; ++g) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] += s_sum[4 * ((g << lpr_log2) + tid) + j];
+      }
+      store4(p, p.sorted[i].x, col, f32x4_a4{acc[0] * p.scale, acc[1] * p.scale, acc[2] * p.scale, acc[3] * p.scale});
+    }
+    __syncthreads();
+  }
 }
 
 // ------------------------------------------------------------ launch -----
@@ -250,17 +370,51 @@ void launch_embed(const EmbedArgs& a, int cus, hipStream_t st) {
     hipLaunchKernelGGL(k_embed<false>, grid, dim3(kEmbThreads), 0, st, a, lpr);
 }
 
-void launch_embed_grad(const EmbedArgs& a, int cus, hipStream_t st) {
-  const int lpr = log2_up((a.D + 3) / 4, 4, 8);
-  const int64_t chunks = (a.D + ((int64_t)4 << lpr) - 1) / ((int64_t)4 << lpr);
-  int rows = 1;  // as many rows a workgroup as leaves 16 workgroups per CU, up to the mask's 64
-  while (rows < 64 && (a.V / (2 * rows)) * chunks >= (int64_t)cus * 16) rows *= 2;
-  // workgroups past the grid's 2^31 - 1: V * D <= 2^40 keeps the count below 2^40 / (64 * 64)
-  const dim3 grid((unsigned)(((a.V + rows - 1) / rows) * chunks));
+// Workspace: the sorted entries (twice if runs are merged), the list of rows
+// with many entries, its length.
+static int64_t sorted_entries(int64_t T) { return (T + kRun - 1) / kRun * kRun; }
+
+int64_t embed_grad_workspace(int64_t T) {
+  const int64_t n = sorted_entries(T);
+  return T == 0 ? 0 : (n > kRun ? 2 * n : n) * 8 + (T / kFew + 1) * 8 + 8;
+}
+
+template <bool BF16>
+static void launch_embed_sums(const EmbedArgs& a, int cus, hipStream_t st) {
+  const int64_t vecs = (a.D + 3) / 4;
+  const int lpr = log2_up((vecs + 3) / 4, 2, 6);  // lanes that cover a row at once, up to a wave
+  const int64_t per = kEmbThreads >> lpr, parts = (vecs + (4 << lpr) - 1) / (4 << lpr);
+  hipLaunchKernelGGL(k_embed_few<BF16>, dim3((unsigned)((a.T + per - 1) / per), (unsigned)parts), dim3(kEmbThreads), 0,
+                     st, a, lpr);
+  if (a.T <= kFew) return;
+  const int lm = log2_up(vecs, 4, 6);
+  const int64_t chunks = (vecs + (1 << lm) - 1) >> lm;
+  hipLaunchKernelGGL(k_embed_many<BF16>, dim3((unsigned)std::min<int64_t>(a.T / kFew * chunks, 2 * cus)), dim3(kManyThreads), 0, st, a, lm,
+                     (uint32_t)chunks);
+}
+
+void launch_embed_grad(const EmbedArgs& args, void* workspace, int cus, hipStream_t st) {
+  EmbedArgs a = args;
+  const int64_t n = sorted_entries(a.T), vecs = (a.V * a.D + 3) / 4;
+  hipLaunchKernelGGL(k_embed_fill, dim3((unsigned)((vecs + kEmbThreads - 1) / kEmbThreads)), dim3(kEmbThreads), 0, st,
+                     static_cast<float*>(a.out), a.V * a.D);
+  if (a.T == 0) return;
+  a.sorted = static_cast<uint2*>(workspace);
+  uint2* other = a.sorted + n;
+  a.many = a.sorted + (n > kRun ? 2 * n : n);
+  a.count = reinterpret_cast<uint32_t*>(a.many + a.T / kFew + 1);
+  int bits = 1;
+  while (a.V >> bits) ++bits;  // keys 0 .. V
+  hipLaunchKernelGGL(k_embed_sort, dim3((unsigned)(n / kRun)), dim3(kSortThreads), 0, st, a, bits);
+  for (int64_t len = kRun; len < n; len *= 2) {
+    hipLaunchKernelGGL(k_embed_merge, dim3((unsigned)(n / kEmbThreads)), dim3(kEmbThreads), 0, st, a.sorted, other, n,
+                       len);
+    std::swap(a.sorted, other);
+  }
   if (a.bf16)
-    hipLaunchKernelGGL(k_embed_grad<true>, grid, dim3(kEmbThreads), 0, st, a, lpr, rows, chunks);
+    launch_embed_sums<true>(a, cus, st);
   else
-    hipLaunchKernelGGL(k_embed_grad<false>, grid, dim3(kEmbThreads), 0, st, a, lpr, rows, chunks);
+    launch_embed_sums<false>(a, cus, st);
 }
 
 }  // namespace nvfp4

@@ -110,10 +110,17 @@ struct EmbedArgs {
   float scale;
   const void* in;      // table [V][D], or dout [T][D]
   void* out;           // [T][D], or the fp32 gradient [V][D]
+  // the gradient's workspace:
+  uint2* sorted;       // (row, position) in the order of rows, then positions
+  uint2* many;         // (first entry, entries) of the rows with many
+  uint32_t* count;     // how many those are
 };
 
+constexpr int64_t kEmbedMaxTokens = INT64_C(1) << 24;  // of the gradient
+
 void launch_embed(const EmbedArgs& a, int cus, hipStream_t st);
-void launch_embed_grad(const EmbedArgs& a, int cus, hipStream_t st);
+int64_t embed_grad_workspace(int64_t T);  // bytes
+void launch_embed_grad(const EmbedArgs& a, void* workspace, int cus, hipStream_t st);
 
 // MXFP4: 32-element blocks of E2M1 codes with E8M0 (power-of-two) scales
 struct MxGemmArgs {

@@ -337,11 +337,15 @@ int nvfp4_embed(const int32_t* tokens, int64_t T, const void* table, int dtype, 
  * Its gradient: grad [V][D] fp32, grad[v] = scale * sum of dout[t] over the t
  * with tokens[t] == v, zeros for a row no token names (every row is written).
  * Sums are fp32 in one fixed order, so results repeat bit for bit.  Tokens
- * outside 0 .. V - 1 add nothing.  With T = 0 tokens and dout may be NULL.
- * Shapes and alignment as nvfp4_embed; dout [T][D] of `dtype`.
+ * outside 0 .. V - 1 add nothing.  workspace is scratch memory of
+ * nvfp4_embed_grad_workspace(T) bytes, whatever it holds (the tokens are
+ * sorted by row there); with T = 0 tokens, dout and workspace may be NULL.
+ * Shapes: 0 <= T < 2^24, 1 <= V <= 2^27, 1 <= D <= 2^18, V * D <= 2^33;
+ * dout [T][D] of `dtype`.  Alignment: one element, workspace 8 bytes.
  */
+int64_t nvfp4_embed_grad_workspace(int64_t T);
 int nvfp4_embed_grad(const int32_t* tokens, int64_t T, const void* dout, int dtype, int64_t V, int64_t D,
-                     float scale, float* grad, void* stream);
+                     float scale, float* grad, void* workspace, void* stream);
 
 /* Static text for a status code. */
 const char* nvfp4_status_string(int status);

@@ -49,7 +49,8 @@ def check_grad(tok, dout, V, scale):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,V,D", [(1, 1, 1), (1, 1000, 64), (5, 3, 7), (64, 64, 64), (257, 30, 63), (1000, 1000, 65),
                                    (4095, 200, 130), (4097, 1000, 256), (8192, 1000, 96), (300, 5000, 1027),
-                                   (2000, 100, 2051), (513, 70000, 80), (9001, 33, 260), (8192, 20000, 1032)])
+                                   (2000, 100, 2051), (513, 70000, 80), (9001, 33, 260), (8192, 20000, 1032), (16384, 50, 16),
+                                   (30000, 3000, 40), (70001, 500, 20)])
 @pytest.mark.parametrize("kind", ["zipf", "even"])
 def test_gradient(T, V, D, dtype, kind):
     tok, g = tokens(T, V, T + V, kind)
@@ -77,7 +78,7 @@ def test_no_tokens():
     tok = torch.empty(0, dtype=torch.int32, device=DEV)
     assert nv.embed(tok, torch.randn(4, 6, device=DEV)).shape == (0, 6)
     grad = torch.full((100, 6), 3.0, device=DEV)
-    nv.nvfp4_embed_grad(tok, torch.empty(0, 6, device=DEV), 1.0, grad)
+    nv.nvfp4_embed_grad(tok, torch.empty(0, 6, device=DEV), 1.0, grad, torch.empty(0, dtype=torch.uint8, device=DEV))
     assert not grad.any()
 
 
@@ -98,8 +99,9 @@ def test_gradient_against_differences():
 @pytest.mark.parametrize("T,V,D", [(100, 50, 5), (100, 50, 67), (1, 1, 1030)])
 def test_nothing_outside_the_outputs_is_written(T, V, D):
     tok, g = tokens(T, V, 1)
+    space = torch.empty(nv.nvfp4_embed_grad_workspace(T), dtype=torch.uint8, device=DEV)
     for rows, call in ((T, lambda o: nv.nvfp4_embed(tok, torch.ones(V, D, device=DEV), 1.0, o)),
-                       (V, lambda o: nv.nvfp4_embed_grad(tok, torch.ones(T, D, device=DEV), 1.0, o))):
+                       (V, lambda o: nv.nvfp4_embed_grad(tok, torch.ones(T, D, device=DEV), 1.0, o, space))):
         buf = torch.full((rows * D + 256,), 7.25, device=DEV)
         call(buf[128:128 + rows * D].view(rows, D))
         assert (buf[:128] == 7.25).all() and (buf[128 + rows * D:] == 7.25).all()
@@ -116,3 +118,19 @@ def test_large_table():
     assert grad.view(-1).count_nonzero().item() == grad[[0, 2 ** 20, 2 ** 21, V - 1]].count_nonzero().item()
     out = nv.embed(tok, grad)
     assert torch.equal(out[1], grad[V - 1]) and torch.equal(out[3], grad[2 ** 21])
+
+
+@pytest.mark.parametrize("T", [700, 9000])
+def test_workspace_contents_do_not_matter(T):
+    V, D = 300, 20
+    tok, g = tokens(T, V, 2)
+    dout = torch.randn(T, D, device=DEV)
+    want, got = nv.embed_grad(tok, dout, V), torch.empty(V, D, device=DEV)
+    size = nv.nvfp4_embed_grad_workspace(T)
+    for fill in (0, 0xFF):
+        nv.nvfp4_embed_grad(tok, dout, 1.0, got, torch.full((size,), fill, dtype=torch.uint8, device=DEV))
+        assert torch.equal(got, want)
+    space = torch.zeros(size // 4, dtype=torch.int32, device=DEV)  # indexes of another call
+    space.copy_(torch.arange(size // 4, device=DEV) % T)
+    nv.nvfp4_embed_grad(tok, dout, 1.0, got, space.view(torch.uint8))
+    assert torch.equal(got, want)

@@ -122,9 +122,11 @@ def test_embed_rejects_bad_tensors(name, bad):
 @pytest.mark.parametrize("name,bad", [
     ("tokens", z(5, dtype=I32)), ("tokens", z(4, dtype=torch.int64)), ("dout", z(4, 6, dtype=torch.float64)),
     ("grad", z(8, 5, dtype=F32)), ("grad", z(8, 6, dtype=BF16)), ("grad", z(48, dtype=F32)),
+    ("workspace", z(8)), ("workspace", z(1 << 17, dtype=I32)),
 ])
 def test_embed_grad_rejects_bad_tensors(name, bad):
-    a = dict(tokens=z(4, dtype=I32), dout=z(4, 6, dtype=BF16), scale=1.0, grad=z(8, 6, dtype=F32))
+    a = dict(tokens=z(4, dtype=I32), dout=z(4, 6, dtype=BF16), scale=1.0, grad=z(8, 6, dtype=F32),
+             workspace=z(nv.nvfp4_embed_grad_workspace(4)))
     with pytest.raises(ValueError, match=name):
         nv.nvfp4_embed_grad(**dict(a, **{name: bad}))
     with pytest.raises(ValueError, match="GPU memory"):
@@ -202,8 +204,8 @@ def c_embed(tok=A, T=4, table=A, dtype=1, V=8, D=6, scale=1.0, out=A):
     return nv.lib().nvfp4_embed(tok, T, table, dtype, V, D, ctypes.c_float(scale), out, None)
 
 
-def c_embed_grad(tok=A, T=4, table=A, dtype=1, V=8, D=6, scale=1.0, out=A):
-    return nv.lib().nvfp4_embed_grad(tok, T, table, dtype, V, D, ctypes.c_float(scale), out, None)
+def c_embed_grad(tok=A, T=4, table=A, dtype=1, V=8, D=6, scale=1.0, out=A, space=A):
+    return nv.lib().nvfp4_embed_grad(tok, T, table, dtype, V, D, ctypes.c_float(scale), out, space, None)
 
 
 @pytest.mark.parametrize("call", [c_embed, c_embed_grad])
@@ -215,3 +217,18 @@ def c_embed_grad(tok=A, T=4, table=A, dtype=1, V=8, D=6, scale=1.0, out=A):
 ])
 def test_c_embed_rejects(call, kw, status):
     assert call(**kw) == status
+
+
+def test_c_embed_grad_rejects():
+    assert c_embed_grad(space=None) == -1
+    assert c_embed_grad(T=1 << 24) == -2
+    assert c_embed_grad(D=(1 << 18) + 1) == -2
+    assert c_embed_grad(V=1 << 20, D=(1 << 13) + 1) == -2
+    assert c_embed_grad(space=off(4)) == -3
+
+
+def test_embed_grad_workspace():
+    size = nv.nvfp4_embed_grad_workspace
+    assert size(0) == 0 and size(-1) == 0 and size(1 << 24) == 0
+    assert size(1) >= 8192 * 8
+    assert size(8193) >= 2 * 16384 * 8 + 8193 // 8 * 8
