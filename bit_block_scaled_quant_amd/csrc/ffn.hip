@@ -130,9 +130,269 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_ffn(FfnArgs p) {
   if (GRAD && p.g.amax) amax_to(p.g, amax);
 }
 
+// ---- large products: the pipelined stages of the 32 x 32 x 16 MFMA ----------
+// A 256 x 32 NT tile of the block takes 32 NT gate and 32 NT up rows: of a
+// wave's NT tile-columns the first half are gate rows and the second half the
+// up rows of the same columns, so acc[i][j] and acc[i][j + NT / 2] hold the
+// two pre-activations of the same elements.  Only the rows that a stage loads
+// differ from the GEMM.
+//
+// RAGGED: M or F end inside a tile, or K inside a pair of stages (K % 64 == 0).  Rows
+// past the end load the last row.  Past the end of K the codes of the row's
+// last chunk stand in and both scales are zero, which makes every product
+// there zero; scale rows are then only 4-byte aligned, so they go through
+// registers, and are written to LDS at the end of the stage.
+template <int NT>
+__device__ __forceinline__ int64_t paired_row(int b, int64_t n0, int64_t F, bool clamp) {
+  const int j = (b % (32 * NT)) / 32, up = j / (NT / 2);
+  int64_t col = n0 + (b / (32 * NT)) * (16 * NT) + (j % (NT / 2)) * 32 + b % 32;
+  if (clamp) col = min(col, F - 1);
+  return col + up * F;
+}
+
+typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+template <int NT, bool RAGGED>
+struct M32Paired {
+  const GemmArgs& g;
+  int64_t m0, n0, F;
+  u32x4_a4 sa, sb;
+
+  __device__ __forceinline__ M32Paired(const GemmArgs& gg, int64_t m, int64_t n, int64_t f)
+      : g(gg), m0(m), n0(n), F(f) {}
+
+  // 16 scale bytes of a row, zeros past the end of K
+  __device__ __forceinline__ u32x4_a4 scale_words(const uint8_t* scales, int64_t row, int64_t k0) const {
+    const uint8_t* s = scales + row * (g.K / 16) + k0 / 16;
+    u32x4_a4 v = {0u, 0u, 0u, 0u};
+    if (k0 + kDirBK <= g.K) {
+      v = *reinterpret_cast<const u32x4_a4*>(s);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k0 + 64 * i < g.K) v[i] = reinterpret_cast<const uint32_t*>(s)[i];
+    }
+    return v;
+  }
+
+  __device__ __forceinline__ void finish(uint8_t* buf) const {
+    if (!RAGGED) return;
+    using L = M32<NT>;
+    *reinterpret_cast<u32x4_a4*>(buf + L::kOffAS + 16 * threadIdx.x) = sa;
+    if (threadIdx.x < 64 * NT) *reinterpret_cast<u32x4_a4*>(buf + L::kOffBS + 16 * threadIdx.x) = sb;
+  }
+
+  template <int U>
+  __device__ __forceinline__ void part(int64_t k0, uint8_t* buf) {
+    using L = M32<NT>;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t kb = g.K / 2, ks = g.K / 16;
+    if (RAGGED && U == 0) {
+      sa = scale_words(g.a_scales, min(m0 + threadIdx.x, g.M - 1), k0);
+      if (threadIdx.x < 64 * NT) sb = scale_words(g.b_scales, paired_row<NT>(threadIdx.x, n0, F, true), k0);
+    }
+    {
+      const int blk = 8 * wave + U, row = 8 * blk + (lane >> 3);
+      const int chunk = (lane & 7) ^ ((row ^ (row >> 3)) & 7);
+      const uint8_t* a0 = g.a_codes + m0 * kb + k0 / 2;
+      uint32_t off;
+      if (RAGGED)
+        off = (uint32_t)(min<int64_t>(row, g.M - 1 - m0) * kb) + min(16 * chunk, (int)min<int64_t>(kb - k0 / 2, 128) - 16);
+      else
+        off = (uint32_t)(row * kb + 16 * chunk);
+      __builtin_amdgcn_global_load_lds((glb_void_t*)(a0 + off), (lds_void_t*)(buf + 1024 * blk), 16, 0, 0);
+    }
+    if (U < 2 * NT) {
+      const int bb = 2 * NT * wave + U, r = lane >> 3;
+      const int chunk = (lane & 7) ^ ((r ^ bb) & 7);  // row 8 bb + r of the tile
+      const uint8_t* b0 = g.b_codes + paired_row<NT>(8 * bb, n0, F, false) * kb + k0 / 2;
+      int64_t off;
+      if (RAGGED)  // (a block that starts past the end steps back to the last row)
+        off = (paired_row<NT>(8 * bb + r, n0, F, true) - paired_row<NT>(8 * bb, n0, F, false)) * kb +
+              min(16 * chunk, (int)min<int64_t>(kb - k0 / 2, 128) - 16);
+      else
+        off = (uint32_t)(r * kb + 16 * chunk);
+      __builtin_amdgcn_global_load_lds((glb_void_t*)(b0 + off), (lds_void_t*)(buf + L::kOffB + 1024 * bb), 16, 0, 0);
+    }
+    if (!RAGGED && U == 0) m32_issue_scales<256>(g.a_scales + m0 * ks + k0 / 16, ks, buf + L::kOffAS);
+    if (!RAGGED && U == 1 && 64 * wave < 64 * NT) {  // wave-uniform
+      const uint8_t* s = g.b_scales + paired_row<NT>(64 * wave + lane, n0, F, false) * ks + k0 / 16;
+      __builtin_amdgcn_global_load_lds((glb_void_t*)s, (lds_void_t*)(buf + L::kOffBS + 1024 * wave), 16, 0, 0);
+    }
+  }
+};
+
+// Two neighbouring columns of bf16 in one word: columns n and n + 1 sit in
+// lanes r and r ^ 1, values k and k + 1 (k even) in rows m and m + 1.  The lane
+// pair swaps one value, so the even lane holds row m's pair of columns and the
+// odd lane row m + 1's.
+__device__ __forceinline__ uint32_t pair_words(float v0, float v1, bool odd) {
+  const uint32_t h0 = bf16_rne(v0), h1 = bf16_rne(v1);
+  const uint32_t other = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? h0 : h1), 0xB1, 0xF, 0xF, true);
+  return odd ? (other | (h1 << 16)) : (h0 | (other << 16));
+}
+
+__device__ __forceinline__ float max_bf16_pair(float m, uint32_t w) {
+  return fmaxf(m, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xFFFF0000u))));
+}
+
+// One 32 x 32 tile of the block, from the two MFMA tiles of its
+// pre-activations.  D layout: lane l, value k -> column l % 32, row
+// 8 * (k / 4) + 4 * (l / 32) + k % 4; mt is row 4 * (l / 32) of the tile, n the
+// lane's column.  PAIRS: bf16, F even and word-aligned buffers, so that two
+// columns are one word.
+template <int ACT, bool GRAD, bool PAIRS>
+__device__ __forceinline__ void m32_emit_tile(const FfnArgs& p, const floatx16& ga, const floatx16& up, float inv_a,
+                                              float inv_b, int64_t mt, int64_t n, float& amax) {
+  if (!PAIRS) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int64_t m = mt + 8 * (k >> 2) + (k & 3);
+      if (m < p.g.M && n < p.F) emit<ACT, GRAD>(p, m, n, (ga[k] * inv_a) * inv_b, (up[k] * inv_a) * inv_b, amax);
+    }
+    return;
+  }
+  const bool odd = threadIdx.x & 1;
+  const int64_t col = n & ~(int64_t)1;
+  uint32_t dw[8];
+  if (GRAD) {
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      const int64_t m = mt + 8 * (k >> 2) + (k & 3) + odd;
+      dw[k / 2] = 0u;
+      if (m < p.g.M && col < p.F)
+        dw[k / 2] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.dh) + m * p.F + col);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 16; k += 2) {
+    const int64_t m = mt + 8 * (k >> 2) + (k & 3) + odd;
+    const float a0 = (ga[k] * inv_a) * inv_b, a1 = (ga[k + 1] * inv_a) * inv_b;
+    const float u0 = (up[k] * inv_a) * inv_b, u1 = (up[k + 1] * inv_a) * inv_b;
+    const bool in = m < p.g.M && col < p.F;
+    if (GRAD) {
+      // dh of the lane's own column in rows m, m + 1 from the pair's words
+      const uint32_t give = odd ? dw[k / 2] << 16 : dw[k / 2] & 0xFFFF0000u;  // what the partner lacks
+      const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);
+      const uint32_t own = odd ? dw[k / 2] & 0xFFFF0000u : dw[k / 2] << 16;
+      const float d0 = __uint_as_float(odd ? got : own), d1 = __uint_as_float(odd ? own : got);
+      float h0, s0, h1, s1;
+      act_both<ACT>(a0, h0, s0);
+      act_both<ACT>(a1, h1, s1);
+      const uint32_t wa = pair_words(d0 * u0 * s0, d1 * u1 * s1, odd), wu = pair_words(d0 * h0, d1 * h1, odd);
+      if (in) {
+        uint16_t* out = static_cast<uint16_t*>(p.out) + m * 2 * p.F + col;
+        *reinterpret_cast<uint32_t*>(out) = wa;
+        *reinterpret_cast<uint32_t*>(out + p.F) = wu;
+        amax = max_bf16_pair(max_bf16_pair(amax, wa), wu);
+      }
+    } else {
+      const uint32_t w = pair_words(act_value<ACT>(a0) * u0, act_value<ACT>(a1) * u1, odd);
+      if (in)
+        __builtin_nontemporal_store(w, reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + m * p.F + col));
+    }
+  }
+}
+
+// the tiles of a wave, one after the other: written as a recursion over the
+// tile's number, since a loop over all of them exceeds what the compiler
+// unrolls, and indexed at run time the accumulators move to scratch memory
+// (the gradient took 8.3 ms instead of 1.4)
+template <int NT, int ACT, bool GRAD, bool PAIRS, int T = 0>
+__device__ __forceinline__ void m32_emit(const FfnArgs& p, const floatx16 (&acc)[4][NT], float inv_a, float inv_b,
+                                         int64_t mt, int64_t n, float& amax) {
+  constexpr int I = T / (NT / 2), J = T % (NT / 2);
+  m32_emit_tile<ACT, GRAD, PAIRS>(p, acc[I][J], acc[I][J + NT / 2], inv_a, inv_b, mt + 32 * I, n + 32 * J, amax);
+  if constexpr (T + 1 < 2 * NT) m32_emit<NT, ACT, GRAD, PAIRS, T + 1>(p, acc, inv_a, inv_b, mt, n, amax);
+}
+
+template <int NT, bool GRAD, bool RAGGED>
+__global__ __launch_bounds__(kGemmThreads, 1) void k_ffn_m32(FfnArgs p, int64_t ntm, int64_t ntn, bool pairs) {
+  using L = M32<NT>;
+  __shared__ __align__(16) uint8_t buf0[L::kStage];
+  __shared__ __align__(16) uint8_t buf1[L::kStage];
+  const int64_t ntl = ntm * ntn, per_xcd = (ntl + 7) / 8;
+  const int64_t t = (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
+  if (t >= ntl) return;  // the whole workgroup
+  // bands of four tile rows, walked column by column, in contiguous runs for
+  // each XCD, as the GEMM's
+  const int64_t band = t / (4 * ntn), rem = t % (4 * ntn), rows = min<int64_t>(4, ntm - band * 4);
+  const int64_t m0 = (band * 4 + rem % rows) * 256, n0 = (rem / rows) * (32 * NT);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int r = lane & 31, gq = lane >> 5;
+
+  floatx16 acc[4][NT];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.f;
+
+  const int64_t nk = (p.g.K + kDirBK - 1) / kDirBK;
+  M32Paired<NT, RAGGED> ld(p.g, m0, n0, p.F);
+  m32_issue(ld, 0, buf0);
+  __syncthreads();
+  M32Frag<NT> f;
+  M32Raw<NT> q;
+  M32Scales<NT> d;
+  m32_read_scales<NT>(buf0, wm, wn, r, gq, d);
+  m32_read_raw<0, NT>(buf0, wm, wn, r, gq, q);
+  m32_unpack<0, 0, NT>(q, d, f);
+  // (the reads past the last stage are of stale data and unused)
+  for (int64_t kt = 0; kt + 1 < nk; kt += 2) {
+    m32_stage<NT>(ld, true, (kt + 1) * kDirBK, buf0, buf1, f, q, d, acc, wm, wn, r, gq);
+    m32_stage<NT>(ld, kt + 2 < nk, (kt + 2) * kDirBK, buf1, buf0, f, q, d, acc, wm, wn, r, gq);
+  }
+  if (RAGGED && (nk & 1)) m32_stage<NT>(ld, false, 0, buf0, buf1, f, q, d, acc, wm, wn, r, gq);
+
+  float amax = 0.0f;
+  const float inv_a = __fdiv_rn(1.0f, p.g.a_ts[0]), inv_b = __fdiv_rn(1.0f, p.g.b_ts[0]);
+  const int64_t mt = m0 + wm * 128 + 4 * gq, n = n0 + wn * (16 * NT) + r;
+  if (p.act == kSilu) {
+    if (pairs)
+      m32_emit<NT, kSilu, GRAD, true>(p, acc, inv_a, inv_b, mt, n, amax);
+    else
+      m32_emit<NT, kSilu, GRAD, false>(p, acc, inv_a, inv_b, mt, n, amax);
+  } else {
+    if (pairs)
+      m32_emit<NT, kGelu, GRAD, true>(p, acc, inv_a, inv_b, mt, n, amax);
+    else
+      m32_emit<NT, kGelu, GRAD, false>(p, acc, inv_a, inv_b, mt, n, amax);
+  }
+  if (GRAD && p.g.amax) amax_to(p.g, amax);
+}
+
+template <int NT, bool GRAD>
+static void launch_m32(const FfnArgs& p, bool ragged, hipStream_t st) {
+  const int64_t ntm = (p.g.M + 255) / 256, ntn = (p.F + 32 * NT - 1) / (32 * NT);
+  const bool pairs = p.bf16 && p.F % 2 == 0 && (uintptr_t)p.out % 4 == 0 && (uintptr_t)p.dh % 4 == 0;
+  const dim3 grid((unsigned)((ntm * ntn + 7) / 8 * 8));
+  if (ragged)
+    hipLaunchKernelGGL((k_ffn_m32<NT, GRAD, true>), grid, dim3(kGemmThreads), 0, st, p, ntm, ntn, pairs);
+  else
+    hipLaunchKernelGGL((k_ffn_m32<NT, GRAD, false>), grid, dim3(kGemmThreads), 0, st, p, ntm, ntn, pairs);
+}
+
 template <bool GRAD>
-static void launch_ffn_t(const FfnArgs& p, int, hipStream_t st) {
+static void launch_ffn_t(const FfnArgs& p, int cus, hipStream_t st) {
   const GemmArgs& g = p.g;
+  // the pipelined stages: 16-byte chunks of codes, 4-byte groups of scales, and
+  // row offsets within 32 bits
+  const bool stages = g.K % 64 == 0 && g.K <= (INT64_C(1) << 24) && (uintptr_t)g.a_codes % 16 == 0 &&
+                      (uintptr_t)g.b_codes % 16 == 0 && (uintptr_t)g.a_scales % 4 == 0 &&
+                      (uintptr_t)g.b_scales % 4 == 0;
+  if (stages && g.M > 128) {
+    const bool whole_k = g.K % (2 * kDirBK) == 0 && (uintptr_t)g.a_scales % 16 == 0 && (uintptr_t)g.b_scales % 16 == 0;
+    const int64_t tiles = ((g.M + 255) / 256) * ((p.F + 127) / 128);
+    if (tiles >= cus)
+      launch_m32<4, GRAD>(p, !(whole_k && g.M % 256 == 0 && p.F % 128 == 0), st);
+    else
+      launch_m32<2, GRAD>(p, !(whole_k && g.M % 256 == 0 && p.F % 64 == 0), st);
+    return;
+  }
   const bool aligned = g.K % kBK == 0 && ((uintptr_t)g.a_codes % 16 == 0) && ((uintptr_t)g.b_codes % 16 == 0) &&
                        ((uintptr_t)g.a_scales % 8 == 0) && ((uintptr_t)g.b_scales % 8 == 0);
   const dim3 grid((unsigned)((p.F + 63) / 64), (unsigned)((g.M + 127) / 128));

@@ -107,6 +107,8 @@ struct M32Plain {
   const GemmArgs& g;
   int64_t m0, n0;
 
+  __device__ __forceinline__ void finish(uint8_t*) const {}
+
   template <int U>
   __device__ __forceinline__ void part(int64_t k0, uint8_t* buf) const {
     using L = M32<NT>;
@@ -183,7 +185,7 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_gemm_m32(GemmArgs g, int64_
       for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.f;
 
   const int64_t nk = g.K / kDirBK;  // even
-  const M32Plain<NT> ld{g, m0, n0};
+  M32Plain<NT> ld{g, m0, n0};
   m32_issue(ld, 0, buf0);
   __syncthreads();
   M32Frag<NT> f;

@@ -334,8 +334,11 @@ __device__ __forceinline__ void m32_issue_scales(const uint8_t* s0, int64_t ks, 
 // all at once, the 24 loads of every wave backed up in the texture unit and
 // stalled the waves' MFMA issue (about 57 cycles per load instruction, by
 // counters).
+// What a loader has to put into buf itself, from registers, it writes in
+// ld.finish(buf), after all eight parts and before the barrier that publishes
+// the stage.
 template <class LOAD>
-__device__ __forceinline__ void m32_issue(const LOAD& ld, int64_t k0, uint8_t* buf) {
+__device__ __forceinline__ void m32_issue(LOAD& ld, int64_t k0, uint8_t* buf) {
   ld.template part<0>(k0, buf);
   ld.template part<1>(k0, buf);
   ld.template part<2>(k0, buf);
@@ -344,6 +347,7 @@ __device__ __forceinline__ void m32_issue(const LOAD& ld, int64_t k0, uint8_t* b
   ld.template part<5>(k0, buf);
   ld.template part<6>(k0, buf);
   ld.template part<7>(k0, buf);
+  ld.finish(buf);
 }
 
 template <int NT>
@@ -472,7 +476,7 @@ __device__ __forceinline__ void m32_pair(const uint8_t* cur, M32Frag<NT>& f, M32
 // flight at a loop back edge, where the compiler's wait insertion would
 // otherwise make the first LDS reads of cur wait for the loads into nxt.
 template <int NT, class LOAD>
-__device__ __forceinline__ void m32_stage(const LOAD& ld, bool issue, int64_t k_issue, const uint8_t* cur,
+__device__ __forceinline__ void m32_stage(LOAD& ld, bool issue, int64_t k_issue, const uint8_t* cur,
                                           uint8_t* nxt, M32Frag<NT>& f, M32Raw<NT>& q, M32Scales<NT>& d,
                                           floatx16 (&acc)[4][NT], int wm, int wn, int r, int gq) {
   M32Raw<NT> qn;
@@ -508,6 +512,7 @@ __device__ __forceinline__ void m32_stage(const LOAD& ld, bool issue, int64_t k_
   m32_unpack<7, 1, NT>(q, d, f1);
   m32_order<0, false, NT>();
   __builtin_amdgcn_sched_barrier(0);
+  if (issue) ld.finish(nxt);
   __syncthreads();  // waits for this wave's loads of nxt (vmcnt(0)), then all waves
   __builtin_amdgcn_sched_barrier(0);
   m32_mfma<NT>(f1, acc);

@@ -98,8 +98,11 @@ def test_block_and_gradient(M, F, K, act, dtype):
 
 
 @pytest.mark.parametrize("act", [nv.SILU, nv.GELU])
-def test_many_tiles(act):  # more tiles than compute units, ragged on every side
-    run(2100, 2736, 832, act, torch.bfloat16)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,F,K", [(2100, 2736, 832), (4096, 2048, 1024), (4000, 2100, 704), (3900, 2303, 512),
+                                   (4352, 2176, 64)])
+def test_many_tiles(M, F, K, act, dtype):  # about one tile for each compute unit, and more; whole and ragged
+    run(M, F, K, act, dtype)
 
 
 @pytest.mark.parametrize("act", [nv.SILU, nv.GELU])
