@@ -365,6 +365,142 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_ffn_m32(FfnArgs p, int64_t 
   if (GRAD && p.g.amax) amax_to(p.g, amax);
 }
 
+// ---- few tokens: the weights are read once ----------------------------------
+// Up to 64 rows of X.  A workgroup owns 16 NR columns (16 NR gate and 16 NR up
+// rows of W) and all of K; its eight waves take every eighth chunk of 256
+// K-elements, straight from memory into registers, the next chunk's loads in
+// flight while the present one multiplies, and join their sums in LDS in the
+// order of the waves.  Lane l of a wave reads row l % 16 of each 16-row tile
+// and the 64 K-elements 64 (l / 16) .. of a chunk: 32 bytes of codes and four
+// scale bytes, which feed eight MFMA slices (X and W use the same map, so the
+// products pair up).  K % 64 == 0: past its end both scales are zero.
+// Bound by the weights' bytes (59 MB at F = 10240, K = 5120).
+constexpr int kSkinnyThreads = 512, kSkinnyWaves = kSkinnyThreads / 64;
+
+template <int T>
+struct SkinnyRows {
+  uint4 q[T][2];
+  uint32_t sc[T];
+};
+
+template <int T>
+__device__ __forceinline__ void skinny_load(const uint8_t* (&codes)[T], const uint8_t* (&scales)[T], int64_t c,
+                                            bool in, SkinnyRows<T>& d) {
+  const int64_t co = in ? c * 128 : 0, so = in ? c * 16 : 0;  // (past the end: the row's start, unused)
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    d.q[t][0] = *reinterpret_cast<const uint4*>(codes[t] + co);
+    d.q[t][1] = *reinterpret_cast<const uint4*>(codes[t] + co + 16);
+    const uint32_t s = *reinterpret_cast<const uint32_t*>(scales[t] + so);
+    d.sc[t] = in ? s : 0u;
+  }
+}
+
+template <int MT, int NR, bool GRAD>
+__global__ __launch_bounds__(kSkinnyThreads, 2) void k_ffn_skinny(FfnArgs p) {
+  constexpr int TW = 2 * NR;  // tiles of W: NR of the gate, NR of the up projection
+  __shared__ __align__(16) float s_acc[kSkinnyWaves][MT * TW][64][4];
+  const GemmArgs& g = p.g;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * NR), kb = g.K / 2, ks = g.K / 16;
+  // the lane's 64 elements of the first chunk; where K is shorter than that,
+  // the first lanes' ones stand in
+  const int part = 64 * lg < g.K ? lg : 0;
+  const uint8_t *wc[TW], *ws[TW], *xc[MT], *xs[MT];
+#pragma unroll
+  for (int t = 0; t < TW; ++t) {
+    const int64_t row = min(n0 + (t % NR) * 16 + li, p.F - 1) + (t / NR) * p.F;
+    wc[t] = g.b_codes + row * kb + 32 * part;
+    ws[t] = g.b_scales + row * ks + 4 * part;
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t row = min<int64_t>(i * 16 + li, g.M - 1);
+    xc[i] = g.a_codes + row * kb + 32 * part;
+    xs[i] = g.a_scales + row * ks + 4 * part;
+  }
+  floatx4 acc[MT][TW];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int t = 0; t < TW; ++t) acc[i][t] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+  const int64_t nc = (g.K + 255) / 256;
+  SkinnyRows<TW> w, wn;
+  SkinnyRows<MT> x, xn;
+  auto load = [&](int64_t c, SkinnyRows<TW>& lw, SkinnyRows<MT>& lx) {
+    const bool in = c * 256 + 64 * lg < g.K;
+    skinny_load<TW>(wc, ws, c, in, lw);
+    skinny_load<MT>(xc, xs, c, in, lx);
+  };
+  if (wave < nc) load(wave, w, x);
+  for (int64_t c = wave; c < nc; c += kSkinnyWaves) {
+    const bool more = c + kSkinnyWaves < nc;  // wave-uniform
+    if (more) load(c + kSkinnyWaves, wn, xn);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      half8 fw[TW], fx[MT];
+#pragma unroll
+      for (int t = 0; t < TW; ++t) fw[t] = unpack8(raw_word(w.q[t][s >> 2], s & 3), scale_h2(w.sc[t] >> (8 * (s >> 1))));
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fx[i] = unpack8(raw_word(x.q[i][s >> 2], s & 3), scale_h2(x.sc[i] >> (8 * (s >> 1))));
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int t = 0; t < TW; ++t) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fx[i], fw[t], acc[i][t], 0, 0, 0);
+    }
+    if (more) {
+      w = wn;
+      x = xn;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int t = 0; t < TW; ++t) *reinterpret_cast<floatx4*>(s_acc[wave][i * TW + t][lane]) = acc[i][t];
+  __syncthreads();
+
+  // wave v joins and emits row tile v / NR, column tile v % NR: lane holds rows
+  // 4 lg .. 4 lg + 3 of column li
+  const float inv_a = __fdiv_rn(1.0f, g.a_ts[0]), inv_b = __fdiv_rn(1.0f, g.b_ts[0]);
+  float amax = 0.0f;
+  for (int v = wave; v < MT * NR; v += kSkinnyWaves) {
+    const int i = v / NR, j = v % NR;
+    floatx4 a = {0.f, 0.f, 0.f, 0.f}, u = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < kSkinnyWaves; ++s) {
+      const floatx4 da = *reinterpret_cast<const floatx4*>(s_acc[s][i * TW + j][lane]);
+      const floatx4 du = *reinterpret_cast<const floatx4*>(s_acc[s][i * TW + j + NR][lane]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        a[k] += da[k];
+        u[k] += du[k];
+      }
+    }
+    const int64_t n = n0 + j * 16 + li;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t m = i * 16 + 4 * lg + k;
+      if (m >= g.M || n >= p.F) continue;
+      if (p.act == kSilu)
+        emit<kSilu, GRAD>(p, m, n, (a[k] * inv_a) * inv_b, (u[k] * inv_a) * inv_b, amax);
+      else
+        emit<kGelu, GRAD>(p, m, n, (a[k] * inv_a) * inv_b, (u[k] * inv_a) * inv_b, amax);
+    }
+  }
+  if (GRAD && g.amax) amax_to(g, amax);
+}
+
+template <int MT, bool GRAD>
+static void launch_skinny(const FfnArgs& p, int cus, hipStream_t st) {
+  // two column tiles a workgroup unpack X half as often; one where that would
+  // leave compute units without a workgroup
+  if (p.F >= (int64_t)32 * cus)
+    hipLaunchKernelGGL((k_ffn_skinny<MT, 2, GRAD>), dim3((unsigned)((p.F + 31) / 32)), dim3(kSkinnyThreads), 0, st, p);
+  else
+    hipLaunchKernelGGL((k_ffn_skinny<MT, 1, GRAD>), dim3((unsigned)((p.F + 15) / 16)), dim3(kSkinnyThreads), 0, st, p);
+}
+
 template <int NT, bool GRAD>
 static void launch_m32(const FfnArgs& p, bool ragged, hipStream_t st) {
   const int64_t ntm = (p.g.M + 255) / 256, ntn = (p.F + 32 * NT - 1) / (32 * NT);
@@ -384,6 +520,17 @@ static void launch_ffn_t(const FfnArgs& p, int cus, hipStream_t st) {
   const bool stages = g.K % 64 == 0 && g.K <= (INT64_C(1) << 24) && (uintptr_t)g.a_codes % 16 == 0 &&
                       (uintptr_t)g.b_codes % 16 == 0 && (uintptr_t)g.a_scales % 4 == 0 &&
                       (uintptr_t)g.b_scales % 4 == 0;
+  if (stages && g.M <= 64) {
+    if (g.M <= 16)
+      launch_skinny<1, GRAD>(p, cus, st);
+    else if (g.M <= 32)
+      launch_skinny<2, GRAD>(p, cus, st);
+    else if (g.M <= 48)
+      launch_skinny<3, GRAD>(p, cus, st);
+    else
+      launch_skinny<4, GRAD>(p, cus, st);
+    return;
+  }
   if (stages && g.M > 128) {
     const bool whole_k = g.K % (2 * kDirBK) == 0 && (uintptr_t)g.a_scales % 16 == 0 && (uintptr_t)g.b_scales % 16 == 0;
     const int64_t tiles = ((g.M + 255) / 256) * ((p.F + 127) / 128);

@@ -97,6 +97,13 @@ def test_block_and_gradient(M, F, K, act, dtype):
     run(M, F, K, act, dtype, seed=M + F)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M", [1, 2, 16, 17, 32, 33, 45, 48, 49, 64])
+@pytest.mark.parametrize("F,K", [(16, 5120), (250, 2112), (8200, 192), (8193, 2304)])
+def test_few_tokens(M, F, K, dtype):
+    run(M, F, K, nv.SILU, dtype, seed=M + K)
+
+
 @pytest.mark.parametrize("act", [nv.SILU, nv.GELU])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("M,F,K", [(2100, 2736, 832), (4096, 2048, 1024), (4000, 2100, 704), (3900, 2303, 512),
