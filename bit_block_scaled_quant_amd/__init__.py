@@ -294,33 +294,70 @@ def nvfp4_quantize_cast_transpose_with_amax(x, rounding, seed, seed_t, codes, sc
         "nvfp4_quantize_cast_transpose_with_amax")
 
 
-def _want_ffn(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, device):
-    _want(x_codes, "x_codes", _U8, device, (M, K // 2))
-    _want(x_scales, "x_scales", _U8, device, (M, K // 16))
-    _want(w_codes, "w_codes", _U8, device, (2 * F, K // 2))
-    _want(w_scales, "w_scales", _U8, device, (2 * F, K // 16))
-    _want(x_tensor_scale, "x_tensor_scale", _F32, device, min_numel=1)
-    _want(w_tensor_scale, "w_tensor_scale", _F32, device, min_numel=1)
+# One token's calls last a few microseconds on the GPU, so the calls below check
+# a well-formed argument with four comparisons and leave the wording of what is
+# wrong to _want.
+def _arg(t, name, dtypes, device, shape):
+    """The address of a tensor argument after the checks of _want."""
+    if not (type(t) is torch.Tensor and t.dtype in dtypes and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _want(t, name, dtypes, device, shape)
+    return t.data_ptr()
+
+
+def _scale_arg(t, name, device):
+    if not (type(t) is torch.Tensor and t.dtype is torch.float32 and t.device == device and t.numel() > 0
+            and t.is_contiguous()):
+        _want(t, name, _F32, device, min_numel=1)
+    return t.data_ptr()
+
+
+def _out_device(t, name):
+    """The device of the output that names the call's device."""
+    if not isinstance(t, torch.Tensor):
+        _want(t, name, _IN, None)
+    return t.device
+
+
+def _gpu_stream(device):
+    """The current stream's handle; raises for a device that is not a GPU."""
+    if device.type != "cuda":
+        raise ValueError("nvfp4: tensors must live in GPU memory (no CPU path)")
+    return _raw_stream(device.index)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _ffn_args(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, device):
+    return (_arg(x_codes, "x_codes", _U8, device, (M, K // 2)),
+            _arg(x_scales, "x_scales", _U8, device, (M, K // 16)),
+            _scale_arg(x_tensor_scale, "x_tensor_scale", device),
+            _arg(w_codes, "w_codes", _U8, device, (2 * F, K // 2)),
+            _arg(w_scales, "w_scales", _U8, device, (2 * F, K // 16)),
+            _scale_arg(w_tensor_scale, "w_tensor_scale", device), M, F, K)
 
 
 def nvfp4_gated_ffn(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, act, h):
-    _want(h, "h", _IN, h.device if isinstance(h, torch.Tensor) else None, (M, F))
-    _want_ffn(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, h.device)
-    _check(lib().nvfp4_gated_ffn(_ptr(x_codes), _ptr(x_scales), _ptr(x_tensor_scale), _ptr(w_codes),
-                                 _ptr(w_scales), _ptr(w_tensor_scale), int(M), int(F), int(K), int(act), _ptr(h),
-                                 _dtype(h), _stream(h)), "nvfp4_gated_ffn")
+    dev = _out_device(h, "h")
+    out = _arg(h, "h", _IN, dev, (M, F))
+    args = _ffn_args(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, dev)
+    rc = lib().nvfp4_gated_ffn(*args, int(act), out, _dtype(h), _gpu_stream(dev))
+    if rc:
+        _check(rc, "nvfp4_gated_ffn")
 
 
 def nvfp4_gated_ffn_grad(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, act, dh,
                          dgu, dgu_amax=None):
-    _want(dgu, "dgu", _IN, dgu.device if isinstance(dgu, torch.Tensor) else None, (M, 2 * F))
-    _want(dh, "dh", (dgu.dtype,), dgu.device, (M, F))
-    _want_ffn(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, dgu.device)
-    _want(dgu_amax, "dgu_amax", _F32, dgu.device, min_numel=1, optional=True)
-    _check(lib().nvfp4_gated_ffn_grad(_ptr(x_codes), _ptr(x_scales), _ptr(x_tensor_scale), _ptr(w_codes),
-                                      _ptr(w_scales), _ptr(w_tensor_scale), int(M), int(F), int(K), int(act),
-                                      _ptr(dh), _ptr(dgu), _dtype(dgu), _ptr(dgu_amax), _stream(dgu)),
-           "nvfp4_gated_ffn_grad")
+    dev = _out_device(dgu, "dgu")
+    out = _arg(dgu, "dgu", _IN, dev, (M, 2 * F))
+    grad = _arg(dh, "dh", (dgu.dtype,), dev, (M, F))
+    args = _ffn_args(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w_tensor_scale, M, F, K, dev)
+    amax = None if dgu_amax is None else _scale_arg(dgu_amax, "dgu_amax", dev)
+    rc = lib().nvfp4_gated_ffn_grad(*args, int(act), grad, out, _dtype(dgu), amax, _gpu_stream(dev))
+    if rc:
+        _check(rc, "nvfp4_gated_ffn_grad")
 
 
 _I32 = (torch.int32,)
@@ -341,32 +378,34 @@ def nvfp4_distill_topk(logits, idx, top, weight, temperature, loss, lse, grad):
     if not isinstance(idx, torch.Tensor) or idx.dim() != 2:
         raise ValueError("nvfp4: idx must be a 2-D tensor")
     K = idx.shape[1]
-    _want(idx, "idx", _I32, dev, (T, K))
-    _want(top, "top", _F32, dev, (T, K))
-    _want(weight, "weight", _F32, dev, (T,), optional=True)
-    _want(loss, "loss", _F32, dev, (T,), optional=True)
-    _want(lse, "lse", _F32, dev, (T,))
-    _want(grad, "grad", (logits.dtype,), dev, (T, V), optional=True)
-    if not logits.is_cuda:
-        raise ValueError("nvfp4: tensors must live in GPU memory (no CPU path)")
-    _check(lib().nvfp4_distill_topk(ctypes.c_void_p(logits.data_ptr()), _dtype(logits), T, V, stride, _ptr(idx),
-                                    _ptr(top), K, _ptr(weight), float(temperature), _ptr(loss), _ptr(lse),
-                                    _ptr(grad), _stream(logits)), "nvfp4_distill_topk")
+    args = (_arg(idx, "idx", _I32, dev, (T, K)), _arg(top, "top", _F32, dev, (T, K)), K,
+            None if weight is None else _arg(weight, "weight", _F32, dev, (T,)), float(temperature),
+            None if loss is None else _arg(loss, "loss", _F32, dev, (T,)), _arg(lse, "lse", _F32, dev, (T,)),
+            None if grad is None else _arg(grad, "grad", (logits.dtype,), dev, (T, V)))
+    rc = lib().nvfp4_distill_topk(logits.data_ptr(), _dtype(logits), T, V, stride, *args, _gpu_stream(dev))
+    if rc:
+        _check(rc, "nvfp4_distill_topk")
 
 
-def _want_tokens(tokens, device):
+def _want_tokens(tokens):
     if not isinstance(tokens, torch.Tensor) or tokens.dim() != 1:
         raise ValueError("nvfp4: tokens must be a 1-D tensor")
-    _want(tokens, "tokens", _I32, device)
     return tokens.shape[0]
 
 
+def _want_rows(x, name):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"nvfp4: {name} must be a 2-D tensor")
+    return x.shape
+
+
 def nvfp4_embed(tokens, table, scale, out):
-    V, D, dev = _want_input(table, "table")
-    T = _want_tokens(tokens, dev)
-    _want(out, "out", (table.dtype,), dev, (T, D))
-    _check(lib().nvfp4_embed(_ptr(tokens), T, _ptr(table), _dtype(table), V, D, float(scale), _ptr(out),
-                             _stream(table)), "nvfp4_embed")
+    T, (V, D), dev = _want_tokens(tokens), _want_rows(table, "table"), table.device
+    args = (_arg(tokens, "tokens", _I32, dev, (T,)), T, _arg(table, "table", _IN, dev, (V, D)), _dtype(table), V, D,
+            float(scale), _arg(out, "out", (table.dtype,), dev, (T, D)))
+    rc = lib().nvfp4_embed(*args, _gpu_stream(dev))
+    if rc:
+        _check(rc, "nvfp4_embed")
 
 
 def nvfp4_embed_grad_workspace(tokens):
@@ -375,15 +414,14 @@ def nvfp4_embed_grad_workspace(tokens):
 
 
 def nvfp4_embed_grad(tokens, dout, scale, grad, workspace):
-    T, D, dev = _want_input(dout, "dout")
-    if _want_tokens(tokens, dev) != T:
-        raise ValueError(f"nvfp4: tokens must have {T} elements, got {tokens.shape[0]}")
-    if not isinstance(grad, torch.Tensor) or grad.dim() != 2:
-        raise ValueError("nvfp4: grad must be a 2-D tensor")
-    _want(grad, "grad", _F32, dev, (grad.shape[0], D))
+    (T, D), dev = _want_rows(dout, "dout"), dout.device
+    V = _want_rows(grad, "grad")[0]
+    args = (_arg(tokens, "tokens", _I32, dev, (T,)), T, _arg(dout, "dout", _IN, dev, (T, D)), _dtype(dout), V, D,
+            float(scale), _arg(grad, "grad", _F32, dev, (V, D)))
     _want(workspace, "workspace", _U8, dev, min_numel=nvfp4_embed_grad_workspace(T))
-    _check(lib().nvfp4_embed_grad(_ptr(tokens), T, _ptr(dout), _dtype(dout), grad.shape[0], D, float(scale),
-                                  _ptr(grad), _ptr(workspace), _stream(dout)), "nvfp4_embed_grad")
+    rc = lib().nvfp4_embed_grad(*args, workspace.data_ptr(), _gpu_stream(dev))
+    if rc:
+        _check(rc, "nvfp4_embed_grad")
 
 
 # ---- convenience wrappers ---------------------------------------------------

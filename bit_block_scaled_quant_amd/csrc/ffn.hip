@@ -366,16 +366,19 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_ffn_m32(FfnArgs p, int64_t 
 }
 
 // ---- few tokens: the weights are read once ----------------------------------
-// Up to 64 rows of X.  A workgroup owns 16 NR columns (16 NR gate and 16 NR up
-// rows of W) and all of K; its eight waves take every eighth chunk of 256
-// K-elements, straight from memory into registers, the next chunk's loads in
-// flight while the present one multiplies, and join their sums in LDS in the
-// order of the waves.  Lane l of a wave reads row l % 16 of each 16-row tile
-// and the 64 K-elements 64 (l / 16) .. of a chunk: 32 bytes of codes and four
-// scale bytes, which feed eight MFMA slices (X and W use the same map, so the
-// products pair up).  K % 64 == 0: past its end both scales are zero.
-// Bound by the weights' bytes (59 MB at F = 10240, K = 5120).
-constexpr int kSkinnyThreads = 512, kSkinnyWaves = kSkinnyThreads / 64;
+// Up to 64 rows of X.  A workgroup owns 16 columns (16 gate and 16 up rows of
+// W, one MFMA tile each) and all of K; its four waves take every fourth chunk
+// of 256 K-elements, straight from memory into registers, the next chunk's
+// loads in flight while the present one multiplies, and join their sums in LDS
+// in the order of the waves.  Lane l of a wave reads row l % 16 of each 16-row
+// tile and the 64 K-elements 64 (l / 16) .. of a chunk: 32 bytes of codes and
+// four scale bytes, which feed eight MFMA slices (X and W use the same map, so
+// the products pair up).  K % 64 == 0: past its end both scales are zero.
+// At F = 10240, K = 5120 one token takes 18.5 us and 45 take 35 (the weights are
+// 59 MB, 12 us of memory time; past 16 tokens the unpack of X, once for every
+// 16 columns, adds about 7 us for each 16 tokens).  32 columns a workgroup take
+// 24 and 36 us (too few workgroups to spread evenly), eight waves 18 and 41.
+constexpr int kSkinnyThreads = 256, kSkinnyWaves = kSkinnyThreads / 64;
 
 template <int T>
 struct SkinnyRows {
@@ -396,20 +399,21 @@ __device__ __forceinline__ void skinny_load(const uint8_t* (&codes)[T], const ui
   }
 }
 
-template <int MT, int NR, bool GRAD>
+template <int MT, bool GRAD>
 __global__ __launch_bounds__(kSkinnyThreads, 2) void k_ffn_skinny(FfnArgs p) {
-  constexpr int TW = 2 * NR;  // tiles of W: NR of the gate, NR of the up projection
+  constexpr int TW = 2;  // a tile of gate rows, a tile of up rows
   __shared__ __align__(16) float s_acc[kSkinnyWaves][MT * TW][64][4];
   const GemmArgs& g = p.g;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * NR), kb = g.K / 2, ks = g.K / 16;
+  const int64_t n0 = (int64_t)blockIdx.x * 16, kb = g.K / 2, ks = g.K / 16;
+  const float ts_a = g.a_ts[0], ts_b = g.b_ts[0];
   // the lane's 64 elements of the first chunk; where K is shorter than that,
   // the first lanes' ones stand in
   const int part = 64 * lg < g.K ? lg : 0;
   const uint8_t *wc[TW], *ws[TW], *xc[MT], *xs[MT];
 #pragma unroll
   for (int t = 0; t < TW; ++t) {
-    const int64_t row = min(n0 + (t % NR) * 16 + li, p.F - 1) + (t / NR) * p.F;
+    const int64_t row = min(n0 + li, p.F - 1) + t * p.F;
     wc[t] = g.b_codes + row * kb + 32 * part;
     ws[t] = g.b_scales + row * ks + 4 * part;
   }
@@ -426,17 +430,14 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void k_ffn_skinny(FfnArgs p) {
     for (int t = 0; t < TW; ++t) acc[i][t] = floatx4{0.f, 0.f, 0.f, 0.f};
 
   const int64_t nc = (g.K + 255) / 256;
-  SkinnyRows<TW> w, wn;
-  SkinnyRows<MT> x, xn;
-  auto load = [&](int64_t c, SkinnyRows<TW>& lw, SkinnyRows<MT>& lx) {
+  SkinnyRows<TW> w0, w1;
+  SkinnyRows<MT> x0, x1;
+  auto load = [&](int64_t c, SkinnyRows<TW>& w, SkinnyRows<MT>& x) {
     const bool in = c * 256 + 64 * lg < g.K;
-    skinny_load<TW>(wc, ws, c, in, lw);
-    skinny_load<MT>(xc, xs, c, in, lx);
+    skinny_load<TW>(wc, ws, c, in, w);
+    skinny_load<MT>(xc, xs, c, in, x);
   };
-  if (wave < nc) load(wave, w, x);
-  for (int64_t c = wave; c < nc; c += kSkinnyWaves) {
-    const bool more = c + kSkinnyWaves < nc;  // wave-uniform
-    if (more) load(c + kSkinnyWaves, wn, xn);
+  auto multiply = [&](const SkinnyRows<TW>& w, const SkinnyRows<MT>& x) {
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
       half8 fw[TW], fx[MT];
@@ -449,10 +450,17 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void k_ffn_skinny(FfnArgs p) {
 #pragma unroll
         for (int t = 0; t < TW; ++t) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fx[i], fw[t], acc[i][t], 0, 0, 0);
     }
-    if (more) {
-      w = wn;
-      x = xn;
-    }
+  };
+  int64_t c = wave;
+  if (c < nc) load(c, w0, x0);
+  while (c < nc) {  // (every condition is wave-uniform)
+    if (c + kSkinnyWaves < nc) load(c + kSkinnyWaves, w1, x1);
+    multiply(w0, x0);
+    c += kSkinnyWaves;
+    if (c >= nc) break;
+    if (c + kSkinnyWaves < nc) load(c + kSkinnyWaves, w0, x0);
+    multiply(w1, x1);
+    c += kSkinnyWaves;
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -460,45 +468,39 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void k_ffn_skinny(FfnArgs p) {
     for (int t = 0; t < TW; ++t) *reinterpret_cast<floatx4*>(s_acc[wave][i * TW + t][lane]) = acc[i][t];
   __syncthreads();
 
-  // wave v joins and emits row tile v / NR, column tile v % NR: lane holds rows
-  // 4 lg .. 4 lg + 3 of column li
-  const float inv_a = __fdiv_rn(1.0f, g.a_ts[0]), inv_b = __fdiv_rn(1.0f, g.b_ts[0]);
+  // wave v joins and emits row tile v: lane holds rows 4 lg .. 4 lg + 3 of
+  // column li
+  const float inv_a = __fdiv_rn(1.0f, ts_a), inv_b = __fdiv_rn(1.0f, ts_b);
   float amax = 0.0f;
-  for (int v = wave; v < MT * NR; v += kSkinnyWaves) {
-    const int i = v / NR, j = v % NR;
-    floatx4 a = {0.f, 0.f, 0.f, 0.f}, u = {0.f, 0.f, 0.f, 0.f};
+  for (int i = wave; i < MT; i += kSkinnyWaves) {
+    floatx4 v[TW];
 #pragma unroll
-    for (int s = 0; s < kSkinnyWaves; ++s) {
-      const floatx4 da = *reinterpret_cast<const floatx4*>(s_acc[s][i * TW + j][lane]);
-      const floatx4 du = *reinterpret_cast<const floatx4*>(s_acc[s][i * TW + j + NR][lane]);
+    for (int t = 0; t < TW; ++t) {
+      v[t] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        a[k] += da[k];
-        u[k] += du[k];
+      for (int s = 0; s < kSkinnyWaves; ++s) {
+        const floatx4 d = *reinterpret_cast<const floatx4*>(s_acc[s][i * TW + t][lane]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[t][k] += d[k];
       }
     }
-    const int64_t n = n0 + j * 16 + li;
+    const int64_t n = n0 + li;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int64_t m = i * 16 + 4 * lg + k;
       if (m >= g.M || n >= p.F) continue;
       if (p.act == kSilu)
-        emit<kSilu, GRAD>(p, m, n, (a[k] * inv_a) * inv_b, (u[k] * inv_a) * inv_b, amax);
+        emit<kSilu, GRAD>(p, m, n, (v[0][k] * inv_a) * inv_b, (v[1][k] * inv_a) * inv_b, amax);
       else
-        emit<kGelu, GRAD>(p, m, n, (a[k] * inv_a) * inv_b, (u[k] * inv_a) * inv_b, amax);
+        emit<kGelu, GRAD>(p, m, n, (v[0][k] * inv_a) * inv_b, (v[1][k] * inv_a) * inv_b, amax);
     }
   }
   if (GRAD && g.amax) amax_to(g, amax);
 }
 
 template <int MT, bool GRAD>
-static void launch_skinny(const FfnArgs& p, int cus, hipStream_t st) {
-  // two column tiles a workgroup unpack X half as often; one where that would
-  // leave compute units without a workgroup
-  if (p.F >= (int64_t)32 * cus)
-    hipLaunchKernelGGL((k_ffn_skinny<MT, 2, GRAD>), dim3((unsigned)((p.F + 31) / 32)), dim3(kSkinnyThreads), 0, st, p);
-  else
-    hipLaunchKernelGGL((k_ffn_skinny<MT, 1, GRAD>), dim3((unsigned)((p.F + 15) / 16)), dim3(kSkinnyThreads), 0, st, p);
+static void launch_skinny(const FfnArgs& p, hipStream_t st) {
+  hipLaunchKernelGGL((k_ffn_skinny<MT, GRAD>), dim3((unsigned)((p.F + 15) / 16)), dim3(kSkinnyThreads), 0, st, p);
 }
 
 template <int NT, bool GRAD>
@@ -522,13 +524,13 @@ static void launch_ffn_t(const FfnArgs& p, int cus, hipStream_t st) {
                       (uintptr_t)g.b_scales % 4 == 0;
   if (stages && g.M <= 64) {
     if (g.M <= 16)
-      launch_skinny<1, GRAD>(p, cus, st);
+      launch_skinny<1, GRAD>(p, st);
     else if (g.M <= 32)
-      launch_skinny<2, GRAD>(p, cus, st);
+      launch_skinny<2, GRAD>(p, st);
     else if (g.M <= 48)
-      launch_skinny<3, GRAD>(p, cus, st);
+      launch_skinny<3, GRAD>(p, st);
     else
-      launch_skinny<4, GRAD>(p, cus, st);
+      launch_skinny<4, GRAD>(p, st);
     return;
   }
   if (stages && g.M > 128) {
