@@ -68,13 +68,12 @@ __device__ __forceinline__ float get(const FfnArgs& p, int64_t idx) {
                 : static_cast<const float*>(p.dh)[idx];
 }
 
-// one element (m, n) of the block from its two pre-activations
+// one element (m, n) of the block from its two pre-activations (d: its dh)
 template <int ACT, bool GRAD>
-__device__ __forceinline__ void emit(const FfnArgs& p, int64_t m, int64_t n, float a, float u, float& amax) {
+__device__ __forceinline__ void emit(const FfnArgs& p, int64_t m, int64_t n, float a, float u, float d, float& amax) {
   if (GRAD) {
     float h, slope;
     act_both<ACT>(a, h, slope);
-    const float d = get(p, m * p.F + n);
     amax = fmaxf(amax, put(p, m * 2 * p.F + n, d * u * slope));
     amax = fmaxf(amax, put(p, (m * 2 + 1) * p.F + n, d * h));
   } else {
@@ -120,10 +119,11 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_ffn(FfnArgs p) {
         const int64_t m = mrow + i * 16 + r, n = ncol + j * 16;
         if (m >= p.g.M || n >= p.F) continue;
         const float a = (acc[i][j][r] * inv_a) * inv_b, u = (acc[i][j + TJ / 2][r] * inv_a) * inv_b;
+        const float d = GRAD ? get(p, m * p.F + n) : 0.0f;
         if (p.act == kSilu)
-          emit<kSilu, GRAD>(p, m, n, a, u, amax);
+          emit<kSilu, GRAD>(p, m, n, a, u, d, amax);
         else
-          emit<kGelu, GRAD>(p, m, n, a, u, amax);
+          emit<kGelu, GRAD>(p, m, n, a, u, d, amax);
       }
     }
   }
@@ -152,7 +152,7 @@ __device__ __forceinline__ int64_t paired_row(int b, int64_t n0, int64_t F, bool
 
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
-template <int NT, bool RAGGED>
+template <int NT, int MT, bool RAGGED>
 struct M32Paired {
   const GemmArgs& g;
   int64_t m0, n0, F;
@@ -177,23 +177,23 @@ struct M32Paired {
 
   __device__ __forceinline__ void finish(uint8_t* buf) const {
     if (!RAGGED) return;
-    using L = M32<NT>;
-    *reinterpret_cast<u32x4_a4*>(buf + L::kOffAS + 16 * threadIdx.x) = sa;
+    using L = M32<NT, MT>;
+    if (threadIdx.x < 64 * MT) *reinterpret_cast<u32x4_a4*>(buf + L::kOffAS + 16 * threadIdx.x) = sa;
     if (threadIdx.x < 64 * NT) *reinterpret_cast<u32x4_a4*>(buf + L::kOffBS + 16 * threadIdx.x) = sb;
   }
 
   template <int U>
   __device__ __forceinline__ void part(int64_t k0, uint8_t* buf) {
-    using L = M32<NT>;
+    using L = M32<NT, MT>;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t kb = g.K / 2, ks = g.K / 16;
     if (RAGGED && U == 0) {
-      sa = scale_words(g.a_scales, min(m0 + threadIdx.x, g.M - 1), k0);
+      if (threadIdx.x < 64 * MT) sa = scale_words(g.a_scales, min(m0 + threadIdx.x, g.M - 1), k0);
       if (threadIdx.x < 64 * NT) sb = scale_words(g.b_scales, paired_row<NT>(threadIdx.x, n0, F, true), k0);
     }
-    {
-      const int blk = 8 * wave + U, row = 8 * blk + (lane >> 3);
+    if (U < 2 * MT) {
+      const int blk = 2 * MT * wave + U, row = 8 * blk + (lane >> 3);
       const int chunk = (lane & 7) ^ ((row ^ (row >> 3)) & 7);
       const uint8_t* a0 = g.a_codes + m0 * kb + k0 / 2;
       uint32_t off;
@@ -215,7 +215,7 @@ struct M32Paired {
         off = (uint32_t)(r * kb + 16 * chunk);
       __builtin_amdgcn_global_load_lds((glb_void_t*)(b0 + off), (lds_void_t*)(buf + L::kOffB + 1024 * bb), 16, 0, 0);
     }
-    if (!RAGGED && U == 0) m32_issue_scales<256>(g.a_scales + m0 * ks + k0 / 16, ks, buf + L::kOffAS);
+    if (!RAGGED && U == 0) m32_issue_scales<64 * MT>(g.a_scales + m0 * ks + k0 / 16, ks, buf + L::kOffAS);
     if (!RAGGED && U == 1 && 64 * wave < 64 * NT) {  // wave-uniform
       const uint8_t* s = g.b_scales + paired_row<NT>(64 * wave + lane, n0, F, false) * ks + k0 / 16;
       __builtin_amdgcn_global_load_lds((glb_void_t*)s, (lds_void_t*)(buf + L::kOffBS + 1024 * wave), 16, 0, 0);
@@ -246,10 +246,19 @@ template <int ACT, bool GRAD, bool PAIRS>
 __device__ __forceinline__ void m32_emit_tile(const FfnArgs& p, const floatx16& ga, const floatx16& up, float inv_a,
                                               float inv_b, int64_t mt, int64_t n, float& amax) {
   if (!PAIRS) {
+    float dh[16];  // all sixteen leave before the first is waited for
+    if (GRAD) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int64_t m = mt + 8 * (k >> 2) + (k & 3);
+        dh[k] = m < p.g.M && n < p.F ? get(p, m * p.F + n) : 0.0f;
+      }
+    }
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       const int64_t m = mt + 8 * (k >> 2) + (k & 3);
-      if (m < p.g.M && n < p.F) emit<ACT, GRAD>(p, m, n, (ga[k] * inv_a) * inv_b, (up[k] * inv_a) * inv_b, amax);
+      if (m < p.g.M && n < p.F)
+        emit<ACT, GRAD>(p, m, n, (ga[k] * inv_a) * inv_b, (up[k] * inv_a) * inv_b, GRAD ? dh[k] : 0.0f, amax);
     }
     return;
   }
@@ -299,68 +308,81 @@ __device__ __forceinline__ void m32_emit_tile(const FfnArgs& p, const floatx16& 
 // tile's number, since a loop over all of them exceeds what the compiler
 // unrolls, and indexed at run time the accumulators move to scratch memory
 // (the gradient took 8.3 ms instead of 1.4)
-template <int NT, int ACT, bool GRAD, bool PAIRS, int T = 0>
-__device__ __forceinline__ void m32_emit(const FfnArgs& p, const floatx16 (&acc)[4][NT], float inv_a, float inv_b,
+template <int NT, int MT, int ACT, bool GRAD, bool PAIRS, int T = 0>
+__device__ __forceinline__ void m32_emit(const FfnArgs& p, const floatx16 (&acc)[MT][NT], float inv_a, float inv_b,
                                          int64_t mt, int64_t n, float& amax) {
   constexpr int I = T / (NT / 2), J = T % (NT / 2);
   m32_emit_tile<ACT, GRAD, PAIRS>(p, acc[I][J], acc[I][J + NT / 2], inv_a, inv_b, mt + 32 * I, n + 32 * J, amax);
-  if constexpr (T + 1 < 2 * NT) m32_emit<NT, ACT, GRAD, PAIRS, T + 1>(p, acc, inv_a, inv_b, mt, n, amax);
+  if constexpr (2 * (T + 1) < MT * NT) m32_emit<NT, MT, ACT, GRAD, PAIRS, T + 1>(p, acc, inv_a, inv_b, mt, n, amax);
 }
 
-template <int NT, bool GRAD, bool RAGGED>
-__global__ __launch_bounds__(kGemmThreads, 1) void k_ffn_m32(FfnArgs p, int64_t ntm, int64_t ntn, bool pairs) {
-  using L = M32<NT>;
+// The tiles of a launch: rows x cols parents, of which it covers np, from
+// parent0, in bands of four parent rows walked column by column and in
+// contiguous runs for each XCD, as the GEMM's.  A parent is one tile, or, where
+// small tiles take what the large ones left (down, across > 1), a large
+// tile's parts one after the other.
+struct M32Grid {
+  int64_t rows, cols, parent0, np;
+  int down, across;  // tiles of a parent
+};
+
+template <int NT, int MT, bool GRAD, bool RAGGED>
+__global__ __launch_bounds__(kGemmThreads, MT == 4 ? 1 : 2) void k_ffn_m32(FfnArgs p, M32Grid gr, bool pairs) {
+  using L = M32<NT, MT>;
   __shared__ __align__(16) uint8_t buf0[L::kStage];
   __shared__ __align__(16) uint8_t buf1[L::kStage];
-  const int64_t ntl = ntm * ntn, per_xcd = (ntl + 7) / 8;
+  const int parts = gr.down * gr.across;
+  const int64_t ntl = gr.np * parts, per_xcd = (ntl + 7) / 8;
   const int64_t t = (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
-  if (t >= ntl) return;  // the whole workgroup
-  // bands of four tile rows, walked column by column, in contiguous runs for
-  // each XCD, as the GEMM's
-  const int64_t band = t / (4 * ntn), rem = t % (4 * ntn), rows = min<int64_t>(4, ntm - band * 4);
-  const int64_t m0 = (band * 4 + rem % rows) * 256, n0 = (rem / rows) * (32 * NT);
+  if (t >= ntl) return;  // the whole workgroup, as below
+  const int64_t u = gr.parent0 + t / parts, band = u / (4 * gr.cols), rem = u % (4 * gr.cols);
+  const int64_t rows = min<int64_t>(4, gr.rows - band * 4);
+  const int part = (int)(t % parts);
+  const int64_t m0 = ((band * 4 + rem % rows) * gr.down + part % gr.down) * L::kBM;
+  const int64_t n0 = ((rem / rows) * gr.across + part / gr.down) * (L::kBN / 2);
+  if (m0 >= p.g.M || n0 >= p.F) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 1, wn = wave & 1;
   const int r = lane & 31, gq = lane >> 5;
 
-  floatx16 acc[4][NT];
+  floatx16 acc[MT][NT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.f;
 
   const int64_t nk = (p.g.K + kDirBK - 1) / kDirBK;
-  M32Paired<NT, RAGGED> ld(p.g, m0, n0, p.F);
+  M32Paired<NT, MT, RAGGED> ld(p.g, m0, n0, p.F);
   m32_issue(ld, 0, buf0);
   __syncthreads();
-  M32Frag<NT> f;
-  M32Raw<NT> q;
-  M32Scales<NT> d;
-  m32_read_scales<NT>(buf0, wm, wn, r, gq, d);
-  m32_read_raw<0, NT>(buf0, wm, wn, r, gq, q);
-  m32_unpack<0, 0, NT>(q, d, f);
+  M32Frag<NT, MT> f;
+  M32Raw<NT, MT> q;
+  M32Scales<NT, MT> d;
+  m32_read_scales<NT, MT>(buf0, wm, wn, r, gq, d);
+  m32_read_raw<0, NT, MT>(buf0, wm, wn, r, gq, q);
+  m32_unpack<0, 0, NT, MT>(q, d, f);
   // (the reads past the last stage are of stale data and unused)
   for (int64_t kt = 0; kt + 1 < nk; kt += 2) {
-    m32_stage<NT>(ld, true, (kt + 1) * kDirBK, buf0, buf1, f, q, d, acc, wm, wn, r, gq);
-    m32_stage<NT>(ld, kt + 2 < nk, (kt + 2) * kDirBK, buf1, buf0, f, q, d, acc, wm, wn, r, gq);
+    m32_stage<NT, MT>(ld, true, (kt + 1) * kDirBK, buf0, buf1, f, q, d, acc, wm, wn, r, gq);
+    m32_stage<NT, MT>(ld, kt + 2 < nk, (kt + 2) * kDirBK, buf1, buf0, f, q, d, acc, wm, wn, r, gq);
   }
-  if (RAGGED && (nk & 1)) m32_stage<NT>(ld, false, 0, buf0, buf1, f, q, d, acc, wm, wn, r, gq);
+  if (RAGGED && (nk & 1)) m32_stage<NT, MT>(ld, false, 0, buf0, buf1, f, q, d, acc, wm, wn, r, gq);
 
   float amax = 0.0f;
   const float inv_a = __fdiv_rn(1.0f, p.g.a_ts[0]), inv_b = __fdiv_rn(1.0f, p.g.b_ts[0]);
-  const int64_t mt = m0 + wm * 128 + 4 * gq, n = n0 + wn * (16 * NT) + r;
+  const int64_t mt = m0 + wm * (32 * MT) + 4 * gq, n = n0 + wn * (16 * NT) + r;
   if (p.act == kSilu) {
     if (pairs)
-      m32_emit<NT, kSilu, GRAD, true>(p, acc, inv_a, inv_b, mt, n, amax);
+      m32_emit<NT, MT, kSilu, GRAD, true>(p, acc, inv_a, inv_b, mt, n, amax);
     else
-      m32_emit<NT, kSilu, GRAD, false>(p, acc, inv_a, inv_b, mt, n, amax);
+      m32_emit<NT, MT, kSilu, GRAD, false>(p, acc, inv_a, inv_b, mt, n, amax);
   } else {
     if (pairs)
-      m32_emit<NT, kGelu, GRAD, true>(p, acc, inv_a, inv_b, mt, n, amax);
+      m32_emit<NT, MT, kGelu, GRAD, true>(p, acc, inv_a, inv_b, mt, n, amax);
     else
-      m32_emit<NT, kGelu, GRAD, false>(p, acc, inv_a, inv_b, mt, n, amax);
+      m32_emit<NT, MT, kGelu, GRAD, false>(p, acc, inv_a, inv_b, mt, n, amax);
   }
   if (GRAD && p.g.amax) amax_to(p.g, amax);
 }
@@ -489,10 +511,11 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void k_ffn_skinny(FfnArgs p) {
     for (int k = 0; k < 4; ++k) {
       const int64_t m = i * 16 + 4 * lg + k;
       if (m >= g.M || n >= p.F) continue;
+      const float d = GRAD ? get(p, m * p.F + n) : 0.0f;
       if (p.act == kSilu)
-        emit<kSilu, GRAD>(p, m, n, (v[0][k] * inv_a) * inv_b, (v[1][k] * inv_a) * inv_b, amax);
+        emit<kSilu, GRAD>(p, m, n, (v[0][k] * inv_a) * inv_b, (v[1][k] * inv_a) * inv_b, d, amax);
       else
-        emit<kGelu, GRAD>(p, m, n, (v[0][k] * inv_a) * inv_b, (v[1][k] * inv_a) * inv_b, amax);
+        emit<kGelu, GRAD>(p, m, n, (v[0][k] * inv_a) * inv_b, (v[1][k] * inv_a) * inv_b, d, amax);
     }
   }
   if (GRAD && g.amax) amax_to(g, amax);
@@ -503,15 +526,24 @@ static void launch_skinny(const FfnArgs& p, hipStream_t st) {
   hipLaunchKernelGGL((k_ffn_skinny<MT, GRAD>), dim3((unsigned)((p.F + 15) / 16)), dim3(kSkinnyThreads), 0, st, p);
 }
 
-template <int NT, bool GRAD>
-static void launch_m32(const FfnArgs& p, bool ragged, hipStream_t st) {
-  const int64_t ntm = (p.g.M + 255) / 256, ntn = (p.F + 32 * NT - 1) / (32 * NT);
+static int64_t tiles_of(int64_t n, int64_t size) { return (n + size - 1) / size; }
+
+template <int NT, int MT, bool GRAD>
+static void launch_m32(const FfnArgs& p, bool whole_k, const M32Grid& gr, hipStream_t st) {
   const bool pairs = p.bf16 && p.F % 2 == 0 && (uintptr_t)p.out % 4 == 0 && (uintptr_t)p.dh % 4 == 0;
-  const dim3 grid((unsigned)((ntm * ntn + 7) / 8 * 8));
+  const bool ragged = !(whole_k && p.g.M % (64 * MT) == 0 && p.F % (32 * NT) == 0);
+  const dim3 grid((unsigned)(tiles_of(gr.np * gr.down * gr.across, 8) * 8));
   if (ragged)
-    hipLaunchKernelGGL((k_ffn_m32<NT, GRAD, true>), grid, dim3(kGemmThreads), 0, st, p, ntm, ntn, pairs);
+    hipLaunchKernelGGL((k_ffn_m32<NT, MT, GRAD, true>), grid, dim3(kGemmThreads), 0, st, p, gr, pairs);
   else
-    hipLaunchKernelGGL((k_ffn_m32<NT, GRAD, false>), grid, dim3(kGemmThreads), 0, st, p, ntm, ntn, pairs);
+    hipLaunchKernelGGL((k_ffn_m32<NT, MT, GRAD, false>), grid, dim3(kGemmThreads), 0, st, p, gr, pairs);
+}
+
+// all tiles of 64 MT x 32 NT
+template <int NT, int MT, bool GRAD>
+static void launch_m32_all(const FfnArgs& p, bool whole_k, hipStream_t st) {
+  const int64_t rows = tiles_of(p.g.M, 64 * MT), cols = tiles_of(p.F, 32 * NT);
+  launch_m32<NT, MT, GRAD>(p, whole_k, M32Grid{rows, cols, 0, rows * cols, 1, 1}, st);
 }
 
 template <bool GRAD>
@@ -533,13 +565,27 @@ static void launch_ffn_t(const FfnArgs& p, int cus, hipStream_t st) {
       launch_skinny<4, GRAD>(p, st);
     return;
   }
-  if (stages && g.M > 128) {
-    const bool whole_k = g.K % (2 * kDirBK) == 0 && (uintptr_t)g.a_scales % 16 == 0 && (uintptr_t)g.b_scales % 16 == 0;
-    const int64_t tiles = ((g.M + 255) / 256) * ((p.F + 127) / 128);
-    if (tiles >= cus)
-      launch_m32<4, GRAD>(p, !(whole_k && g.M % 256 == 0 && p.F % 128 == 0), st);
-    else
-      launch_m32<2, GRAD>(p, !(whole_k && g.M % 256 == 0 && p.F % 64 == 0), st);
+  if (stages) {
+    const bool whole_k =
+        g.K % (2 * kDirBK) == 0 && (uintptr_t)g.a_scales % 16 == 0 && (uintptr_t)g.b_scales % 16 == 0;
+    // 256 x 128 tiles multiply fastest (1.28 PFLOP/s against 1.08 for 128 x 64,
+    // two workgroups a CU, and 0.83 for 64 x 64), but a CU without a tile, or
+    // with one more than the others, costs a whole tile's time.  So they take
+    // whole rounds of the CUs, and what is left if it fills more than half of
+    // them; else it goes as 128 x 64, which two a CU finish in 0.6 of a
+    // tile's time (M = 1024, F = 10240: 245 us in whole tiles, 220 in small
+    // ones).  Where 64 x 64 tiles do not outnumber the CUs, each CU's share is
+    // smallest with those (M = F = K = 1024: 10.7 us against 13.2 and 30.8).
+    const int64_t rows = tiles_of(g.M, 256), cols = tiles_of(p.F, 128), all = rows * cols;
+    if (tiles_of(g.M, 64) * tiles_of(p.F, 64) <= cus) {
+      launch_m32_all<2, 1, GRAD>(p, whole_k, st);
+    } else if (2 * all <= cus) {
+      launch_m32_all<2, 2, GRAD>(p, whole_k, st);
+    } else {
+      const int64_t left = all % cus, big = 2 * left > cus ? all : all - left;
+      launch_m32<4, 4, GRAD>(p, whole_k, M32Grid{rows, cols, 0, big, 1, 1}, st);
+      if (big < all) launch_m32<2, 2, GRAD>(p, whole_k, M32Grid{rows, cols, big, all - big, 2, 2}, st);
+    }
     return;
   }
   const bool aligned = g.K % kBK == 0 && ((uintptr_t)g.a_codes % 16 == 0) && ((uintptr_t)g.b_codes % 16 == 0) &&

@@ -195,9 +195,9 @@ __global__ __launch_bounds__(kGemmThreads, 1) void k_gemm_m32(GemmArgs g, int64_
   m32_read_raw<0, NT>(buf0, wm, wn, r, gq, q);
   m32_unpack<0, 0, NT>(q, d, f);
   for (int64_t kt = 0; kt < nk; kt += 2) {
-    m32_stage<NT>(ld, true, (kt + 1) * kDirBK, buf0, buf1, f, q, d, acc, wm, wn, r, gq);
+    m32_stage<NT, 4>(ld, true, (kt + 1) * kDirBK, buf0, buf1, f, q, d, acc, wm, wn, r, gq);
     // on the last stage the reads of buf0 at its end are of stale data and unused
-    m32_stage<NT>(ld, kt + 2 < nk, (kt + 2) * kDirBK, buf1, buf0, f, q, d, acc, wm, wn, r, gq);
+    m32_stage<NT, 4>(ld, kt + 2 < nk, (kt + 2) * kDirBK, buf1, buf0, f, q, d, acc, wm, wn, r, gq);
   }
 
   // D layout of the 32 x 32 MFMA: lane l, value k -> column l % 32, row

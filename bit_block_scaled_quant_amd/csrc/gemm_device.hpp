@@ -298,21 +298,22 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 // NT = 32-column MFMA tiles per wave along N: 4 for a 256 x 256 workgroup
 // tile; 2 (256 x 128) or 1 (256 x 64) for the last, partial wave of tiles.
-template <int NT>
+// MT = 32-row MFMA tiles per wave along M: 4, or fewer for smaller tiles.
+template <int NT, int MT = 4>
 struct M32 {
-  static constexpr int kBN = 64 * NT;                 // tile width
-  static constexpr int kOffB = 256 * kDirRow;         // B codes after 32 KB of A codes
-  static constexpr int kOffAS = kOffB + kBN * kDirRow;  // A scales, 4 KB
-  static constexpr int kOffBS = kOffAS + 4096;          // B scales, NT KB
+  static constexpr int kBM = 64 * MT, kBN = 64 * NT;  // tile height and width
+  static constexpr int kOffB = kBM * kDirRow;         // B codes after the A codes
+  static constexpr int kOffAS = kOffB + kBN * kDirRow;  // A scales, MT KB
+  static constexpr int kOffBS = kOffAS + 1024 * MT;     // B scales, NT KB
   static constexpr int kStage = kOffBS + 1024 * NT;
 };
 
-template <int NT>
-struct M32Frag { half8 a[4], b[NT]; };
-template <int NT>
-struct M32Raw { uint4 a[4], b[NT]; };  // blocks 8g + 2Q (.x, .y) and 8g + 2Q + 1 (.z, .w)
-template <int NT>
-struct M32Scales { uint4 a[2], b[(NT + 1) / 2]; };  // dword 2i + q: blocks 8g + 4q .. + 3 of tile-row i
+template <int NT, int MT = 4>
+struct M32Frag { half8 a[MT], b[NT]; };
+template <int NT, int MT = 4>
+struct M32Raw { uint4 a[MT], b[NT]; };  // blocks 8g + 2Q (.x, .y) and 8g + 2Q + 1 (.z, .w)
+template <int NT, int MT = 4>
+struct M32Scales { uint2 a[MT], b[NT]; };  // blocks 8g .. 8g + 3 (.x) and 8g + 4 .. 8g + 7 (.y)
 
 // A stage's scale bytes sit in LDS in their global order: row r's 16 bytes
 // (blocks 0 .. 15 of the stage) at 16 r.  A wave loads 64 rows with one
@@ -350,70 +351,57 @@ __device__ __forceinline__ void m32_issue(LOAD& ld, int64_t k0, uint8_t* buf) {
   ld.finish(buf);
 }
 
-template <int NT>
+template <int NT, int MT = 4>
 __device__ __forceinline__ void m32_read_scales(const uint8_t* buf, int wm, int wn, int r, int gq,
-                                                M32Scales<NT>& d) {
-  using L = M32<NT>;
-  // tile-row i of A is row wm * 128 + 32 i + r; lane group gq takes blocks
+                                                M32Scales<NT, MT>& d) {
+  using L = M32<NT, MT>;
+  // tile-row i of A is row wm * 32 MT + 32 i + r; lane group gq takes blocks
   // 8 gq .. 8 gq + 7, i.e. bytes 8 gq .. 8 gq + 7 of the row (a read
   // instruction covers 512 contiguous bytes: no bank conflicts)
-  const uint8_t* pa = buf + L::kOffAS + 16 * (wm * 128 + r) + 8 * gq;
+  const uint8_t* pa = buf + L::kOffAS + 16 * (wm * 32 * MT + r) + 8 * gq;
   const uint8_t* pb = buf + L::kOffBS + 16 * (wn * 32 * NT + r) + 8 * gq;
-  uint2 ra[4], rb[NT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) ra[i] = *reinterpret_cast<const uint2*>(pa + 16 * 32 * i);
+  for (int i = 0; i < MT; ++i) d.a[i] = *reinterpret_cast<const uint2*>(pa + 16 * 32 * i);
 #pragma unroll
-  for (int j = 0; j < NT; ++j) rb[j] = *reinterpret_cast<const uint2*>(pb + 16 * 32 * j);
-  d.a[0] = make_uint4(ra[0].x, ra[0].y, ra[1].x, ra[1].y);
-  d.a[1] = make_uint4(ra[2].x, ra[2].y, ra[3].x, ra[3].y);
-#pragma unroll
-  for (int k = 0; k < (NT + 1) / 2; ++k) {
-    const uint2 hi = 2 * k + 1 < NT ? rb[2 * k + 1 < NT ? 2 * k + 1 : 0] : make_uint2(0u, 0u);
-    d.b[k] = make_uint4(rb[2 * k].x, rb[2 * k].y, hi.x, hi.y);
-  }
+  for (int j = 0; j < NT; ++j) d.b[j] = *reinterpret_cast<const uint2*>(pb + 16 * 32 * j);
 }
 
 // raw codes of blocks 8g + 2Q and 8g + 2Q + 1 (one 16-byte chunk) for the
 // lane's four A and NT B rows; the eight rows of a swizzle group hit eight
 // distinct chunk positions, so a 16-byte read is free of bank conflicts
-template <int Q, int NT>
+template <int Q, int NT, int MT = 4>
 __device__ __forceinline__ void m32_read_raw(const uint8_t* buf, int wm, int wn, int r, int gq,
-                                             M32Raw<NT>& q) {
+                                             M32Raw<NT, MT>& q) {
   const int c = 4 * gq + Q;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q.a[i] = *reinterpret_cast<const uint4*>(buf + dswz(wm * 128 + i * 32 + r, c));
+  for (int i = 0; i < MT; ++i) q.a[i] = *reinterpret_cast<const uint4*>(buf + dswz(wm * 32 * MT + i * 32 + r, c));
 #pragma unroll
   for (int j = 0; j < NT; ++j)
-    q.b[j] = *reinterpret_cast<const uint4*>(buf + M32<NT>::kOffB + dswz(wn * 32 * NT + j * 32 + r, c));
+    q.b[j] = *reinterpret_cast<const uint4*>(buf + M32<NT, MT>::kOffB + dswz(wn * 32 * NT + j * 32 + r, c));
 }
 
 __device__ __forceinline__ uint32_t raw_word(const uint4& v, int k) {
   return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
 }
 
-__device__ __forceinline__ uint32_t m32_dword(const uint4& v0, const uint4& v1, int k) {
-  return k == 0 ? v0.x : k == 1 ? v0.y : k == 2 ? v0.z : k == 3 ? v0.w : k == 4 ? v1.x : k == 5 ? v1.y
-       : k == 6 ? v1.z : v1.w;
-}
-
 // step (P, S): half S of block 8g + P
-template <int P, int S, int NT>
-__device__ __forceinline__ void m32_unpack(const M32Raw<NT>& q, const M32Scales<NT>& d, M32Frag<NT>& f) {
+template <int P, int S, int NT, int MT = 4>
+__device__ __forceinline__ void m32_unpack(const M32Raw<NT, MT>& q, const M32Scales<NT, MT>& d, M32Frag<NT, MT>& f) {
   constexpr int kw = 2 * (P & 1) + S;  // word of the 16-byte chunk
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MT; ++i)
     f.a[i] = unpack8(raw_word(q.a[i], kw),
-                     scale_h2(m32_dword(d.a[0], d.a[1], 2 * i + (P >> 2)) >> (8 * (P & 3))));
+                     scale_h2((P < 4 ? d.a[i].x : d.a[i].y) >> (8 * (P & 3))));
 #pragma unroll
   for (int j = 0; j < NT; ++j)
     f.b[j] = unpack8(raw_word(q.b[j], kw),
-                     scale_h2(m32_dword(d.b[0], d.b[(NT + 1) / 2 - 1], 2 * j + (P >> 2)) >> (8 * (P & 3))));
+                     scale_h2((P < 4 ? d.b[j].x : d.b[j].y) >> (8 * (P & 3))));
 }
 
-template <int NT>
-__device__ __forceinline__ void m32_mfma(const M32Frag<NT>& f, floatx16 (&acc)[4][NT]) {
+template <int NT, int MT = 4>
+__device__ __forceinline__ void m32_mfma(const M32Frag<NT, MT>& f, floatx16 (&acc)[MT][NT]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j)
       acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
@@ -422,8 +410,9 @@ __device__ __forceinline__ void m32_mfma(const M32Frag<NT>& f, floatx16 (&acc)[4
 // Instruction order of one step of 4 NT MFMAs; READS groups of LDS reads ride
 // on the first MFMAs; with DEP the unpack waits on them behind a few MFMAs.
 // A step's unpack is about 10 VALU per fragment (4 + NT fragments).
-template <int READS, bool DEP, int NT>
+template <int READS, bool DEP, int NT, int MT = 4>
 __device__ __forceinline__ void m32_order() {
+  if (MT < 4) return;  // smaller tiles leave a second workgroup to a CU, whose waves fill in
   constexpr int kMfma = 4 * NT;
 #pragma unroll
   for (int k = 0; k < READS; ++k) {
@@ -446,25 +435,25 @@ __device__ __forceinline__ void m32_order() {
 // pair P of a stage: steps 2P and 2P + 1.  In: f = step (P, 0), q = raw of
 // quad P / 2 (pairs P & ~1 and P | 1).  An even pair also reads the next
 // quad into qn; an odd pair hands it over.
-template <int P, int NT>
-__device__ __forceinline__ void m32_pair(const uint8_t* cur, M32Frag<NT>& f, M32Raw<NT>& q, M32Raw<NT>& qn,
-                                         const M32Scales<NT>& d, floatx16 (&acc)[4][NT], int wm, int wn,
+template <int P, int NT, int MT = 4>
+__device__ __forceinline__ void m32_pair(const uint8_t* cur, M32Frag<NT, MT>& f, M32Raw<NT, MT>& q, M32Raw<NT, MT>& qn,
+                                         const M32Scales<NT, MT>& d, floatx16 (&acc)[MT][NT], int wm, int wn,
                                          int r, int gq) {
   constexpr bool kRead = (P & 1) == 0 && P < 6;
-  M32Frag<NT> f1;
-  m32_mfma<NT>(f, acc);
-  if (kRead) m32_read_raw<P / 2 + 1, NT>(cur, wm, wn, r, gq, qn);
-  m32_unpack<P, 1, NT>(q, d, f1);
-  m32_order<kRead ? 4 + NT : 0, false, NT>();
+  M32Frag<NT, MT> f1;
+  m32_mfma<NT, MT>(f, acc);
+  if (kRead) m32_read_raw<P / 2 + 1, NT, MT>(cur, wm, wn, r, gq, qn);
+  m32_unpack<P, 1, NT, MT>(q, d, f1);
+  m32_order<kRead ? 4 + NT : 0, false, NT, MT>();
   __builtin_amdgcn_sched_barrier(0);
-  m32_mfma<NT>(f1, acc);
+  m32_mfma<NT, MT>(f1, acc);
   if (P & 1) {
-    m32_unpack<P + 1, 0, NT>(qn, d, f);
+    m32_unpack<P + 1, 0, NT, MT>(qn, d, f);
     q = qn;
   } else {
-    m32_unpack<P + 1, 0, NT>(q, d, f);
+    m32_unpack<P + 1, 0, NT, MT>(q, d, f);
   }
-  m32_order<0, false, NT>();
+  m32_order<0, false, NT, MT>();
   __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -475,51 +464,51 @@ __device__ __forceinline__ void m32_pair(const uint8_t* cur, M32Frag<NT>& f, M32
 // barrier before the last step waits for those loads.  No load is then in
 // flight at a loop back edge, where the compiler's wait insertion would
 // otherwise make the first LDS reads of cur wait for the loads into nxt.
-template <int NT, class LOAD>
+template <int NT, int MT, class LOAD>
 __device__ __forceinline__ void m32_stage(LOAD& ld, bool issue, int64_t k_issue, const uint8_t* cur,
-                                          uint8_t* nxt, M32Frag<NT>& f, M32Raw<NT>& q, M32Scales<NT>& d,
-                                          floatx16 (&acc)[4][NT], int wm, int wn, int r, int gq) {
-  M32Raw<NT> qn;
-  m32_pair<0, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
+                                          uint8_t* nxt, M32Frag<NT, MT>& f, M32Raw<NT, MT>& q, M32Scales<NT, MT>& d,
+                                          floatx16 (&acc)[MT][NT], int wm, int wn, int r, int gq) {
+  M32Raw<NT, MT> qn;
+  m32_pair<0, NT, MT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
   if (issue) {
     ld.template part<0>(k_issue, nxt);
     ld.template part<1>(k_issue, nxt);
   }
   __builtin_amdgcn_sched_barrier(0);
-  m32_pair<1, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
+  m32_pair<1, NT, MT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
   if (issue) {
     ld.template part<2>(k_issue, nxt);
     ld.template part<3>(k_issue, nxt);
   }
   __builtin_amdgcn_sched_barrier(0);
-  m32_pair<2, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
+  m32_pair<2, NT, MT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
   if (issue) {
     ld.template part<4>(k_issue, nxt);
     ld.template part<5>(k_issue, nxt);
   }
   __builtin_amdgcn_sched_barrier(0);
-  m32_pair<3, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
+  m32_pair<3, NT, MT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
   if (issue) {
     ld.template part<6>(k_issue, nxt);
     ld.template part<7>(k_issue, nxt);
   }
   __builtin_amdgcn_sched_barrier(0);
-  m32_pair<4, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
-  m32_pair<5, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
-  m32_pair<6, NT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
-  M32Frag<NT> f1;
-  m32_mfma<NT>(f, acc);
-  m32_unpack<7, 1, NT>(q, d, f1);
-  m32_order<0, false, NT>();
+  m32_pair<4, NT, MT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
+  m32_pair<5, NT, MT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
+  m32_pair<6, NT, MT>(cur, f, q, qn, d, acc, wm, wn, r, gq);
+  M32Frag<NT, MT> f1;
+  m32_mfma<NT, MT>(f, acc);
+  m32_unpack<7, 1, NT, MT>(q, d, f1);
+  m32_order<0, false, NT, MT>();
   __builtin_amdgcn_sched_barrier(0);
   if (issue) ld.finish(nxt);
   __syncthreads();  // waits for this wave's loads of nxt (vmcnt(0)), then all waves
   __builtin_amdgcn_sched_barrier(0);
-  m32_mfma<NT>(f1, acc);
-  m32_read_scales<NT>(nxt, wm, wn, r, gq, d);
-  m32_read_raw<0, NT>(nxt, wm, wn, r, gq, q);
-  m32_unpack<0, 0, NT>(q, d, f);
-  m32_order<NT == 4 ? 6 : 5, true, NT>();
+  m32_mfma<NT, MT>(f1, acc);
+  m32_read_scales<NT, MT>(nxt, wm, wn, r, gq, d);
+  m32_read_raw<0, NT, MT>(nxt, wm, wn, r, gq, q);
+  m32_unpack<0, 0, NT, MT>(q, d, f);
+  m32_order<NT == 4 ? 6 : 5, true, NT, MT>();
   __builtin_amdgcn_sched_barrier(0);
 }
 
