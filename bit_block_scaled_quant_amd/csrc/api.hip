@@ -334,9 +334,12 @@ int nvfp4_distill_topk(const void* logits, int dtype, int64_t T, int64_t V, int6
       !aligned(lse, 4) || !aligned(grad, e))
     return NVFP4_ERR_ALIGN;
   if (T == 0) return NVFP4_OK;
+  int cus = 0;
+  int st = device_cus(&cus);
+  if (st) return st;
   nvfp4::DistillArgs a{logits, dtype == NVFP4_BF16, T, V, stride, idx, top, (int)K, weight, temperature, loss, lse,
                        grad};
-  nvfp4::launch_distill(a, (hipStream_t)stream);
+  nvfp4::launch_distill(a, cus, (hipStream_t)stream);
   return check_launch("nvfp4_distill_topk");
 }
 

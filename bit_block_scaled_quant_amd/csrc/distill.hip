@@ -10,15 +10,14 @@
 // One workgroup per row.  The maximum and the sum of exponentials are taken
 // in one pass (each thread keeps its own pair and rescales its sum when its
 // maximum grows), then the gradient is written densely and the few entries
-// of the teacher are corrected.  All statistics are fp32; every reduction has
-// a fixed order, so results repeat bit for bit.
+// of the teacher are corrected.  For loss and gradient together the row stays
+// in registers between the two passes where it fits.  All statistics are
+// fp32; every reduction has a fixed order, so results repeat bit for bit.
 #include "internal.hpp"
 #include "nvfp4_device.hpp"
 
 namespace nvfp4 {
 
-constexpr int kDistThreads = 1024;
-constexpr int kDistWaves = kDistThreads / 64;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // rows start at any element, so vectors are only element-aligned
@@ -53,10 +52,17 @@ __device__ __forceinline__ float dist_at(const char* row, int64_t i) {
   return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
 }
 
+// two fp32 values rounded to nearest-even bf16 in one word (NaN stays NaN)
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 template <bool BF16>
 __device__ __forceinline__ void dist_put(char* row, int64_t i, float v) {
   if (BF16)
-    reinterpret_cast<uint16_t*>(row)[i] = (uint16_t)bf16_rne(v);
+    reinterpret_cast<uint16_t*>(row)[i] = (uint16_t)bf16_pair(v, 0.0f);
   else
     reinterpret_cast<float*>(row)[i] = v;
 }
@@ -85,9 +91,15 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-// N values into a thread's running pair: one rescale for all of them.  The
-// difference to the maximum is rounded before it is scaled, so the terms that
-// carry the sum (x near m) are the precise ones.
+// exp2((x - ref) c + d).  The difference to the maximum is rounded before it is
+// scaled, so the terms that carry a sum (x near the maximum) are the precise
+// ones, and rows of the type's lowest value do not overflow.
+struct Exp {
+  float ref, c, d;
+  __device__ __forceinline__ float operator()(float x) const { return exp2_hw(__builtin_fmaf(x - ref, c, d)); }
+};
+
+// N values into a thread's running pair: one rescale for all of them.
 template <int N>
 __device__ __forceinline__ void online(MaxSum& t, const float (&x)[N], float c) {
   float m = t.m;
@@ -101,49 +113,91 @@ __device__ __forceinline__ void online(MaxSum& t, const float (&x)[N], float c) 
   t.s = s;
 }
 
-template <bool BF16, bool LOSS, bool GRAD>
-__global__ __launch_bounds__(kDistThreads) void k_distill(DistillArgs p) {
-  constexpr int N = Vec16<BF16>::kN;
-  __shared__ float s_red[3][kDistWaves];
+// the block's sum of one value a wave (all threads call; s is scratch)
+template <int WAVES>
+__device__ __forceinline__ float block_sum(float v, float* s) {
+  v = wave_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float all = 0.0f;
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) all += s[i];
+  return all;
+}
+
+// HOLD: 16-byte vectors of the row that a thread keeps in registers (0: the
+// row is read again for the gradient).
+template <bool BF16, int TH, int HOLD, bool LOSS, bool GRAD>
+__global__ __launch_bounds__(TH, TH == 1024 ? 4 : 1) void k_distill(DistillArgs p) {
+  constexpr int N = Vec16<BF16>::kN, WAVES = TH / 64;
+  __shared__ float s_red[3][WAVES];
   __shared__ int32_t s_idx[kDistillMaxK];
-  __shared__ float s_p[kDistillMaxK];
+  __shared__ float s_p[kDistillMaxK], s_z[kDistillMaxK];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x;
   const char* x = static_cast<const char*>(p.logits) + row * p.stride * (BF16 ? 2 : 4);
   const int64_t nvec = p.V / N;
   const float c = kLog2e / p.temperature;
+  const bool tail = nvec * N + tid < p.V;
 
-  // the teacher's entry of this thread (K <= kDistThreads)
-  const bool mine = tid < p.K;
-  int32_t at = -1;
-  float t = -INFINITY, z = 0.0f;
-  if (mine) {
-    at = p.idx[row * p.K + tid];
-    if (at < 0 || at >= p.V) at = -1;
-    if (at >= 0) {
-      t = p.top[row * p.K + tid] / p.temperature;
-      z = dist_at<BF16>(x, at);
+  constexpr uint32_t kNone = BF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+  u32x4 held[HOLD > 0 ? HOLD : 1];
+  if (HOLD > 0) {
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k) {
+      held[k] = u32x4{kNone, kNone, kNone, kNone};
+      if (tid + k * TH < nvec) held[k] = dist_load<BF16>(x, tid + k * TH);
     }
-    s_idx[tid] = at;
+  }
+  const float last = tail ? dist_at<BF16>(x, nvec * N + tid) : -INFINITY;
+
+  // the teacher's entries: present ones' top / tau in s_p, their logits in s_z
+  float th = -INFINITY;
+  for (int j = tid; j < p.K; j += TH) {
+    int32_t at = p.idx[row * p.K + j];
+    const float t = p.top[row * p.K + j] / p.temperature;
+    if (at < 0 || at >= p.V) at = -1;
+    s_idx[j] = at;
+    s_p[j] = at >= 0 ? t : -INFINITY;
+    s_z[j] = at >= 0 ? dist_at<BF16>(x, at) : 0.0f;
+    th = fmaxf(th, s_p[j]);
   }
 
   MaxSum st{-INFINITY, 0.0f};
   if (LOSS) {
-    for (int64_t v = tid; v < nvec; v += kDistThreads) {
-      const u32x4 w = dist_load<BF16>(x, v);
+    const auto add = [&](const u32x4& w) {
       float e[N];
 #pragma unroll
       for (int k = 0; k < N; ++k) e[k] = dist_elem<BF16>(w, k);
       online(st, e, c);
+    };
+    if (HOLD > 0) {
+#pragma unroll
+      for (int k = 0; k < HOLD; ++k) {
+        add(held[k]);
+        // opaque from here on: otherwise the unpacked values are kept for the
+        // gradient beside the packed ones, and spill
+        asm volatile("" : "+v"(held[k]));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+      int64_t v = tid;
+      for (; v + 3 * TH < nvec; v += 4 * TH) {  // four loads in flight
+        u32x4 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = dist_load<BF16>(x, v + k * TH);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) add(w[k]);
+      }
+      for (; v < nvec; v += TH) add(dist_load<BF16>(x, v));
     }
-    if (nvec * N + tid < p.V) {
-      const float e[1] = {dist_at<BF16>(x, nvec * N + tid)};
-      online(st, e, c);
-    }
+    const float e[1] = {last};
+    online(st, e, c);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) st = join(st, MaxSum{__shfl_xor(st.m, off), __shfl_xor(st.s, off)}, c);
   }
-  const float th = wave_max(t);
+  th = wave_max(th);
   if (lane == 0) {
     s_red[0][wave] = st.m;
     s_red[1][wave] = st.s;
@@ -151,91 +205,134 @@ __global__ __launch_bounds__(kDistThreads) void k_distill(DistillArgs p) {
   }
   __syncthreads();
   float high = -INFINITY;
-  st = MaxSum{-INFINITY, 0.0f};
+  if (LOSS) {  // joined at the block's maximum: one exponential a wave
+    float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kDistWaves; ++i) {
-    if (LOSS) st = join(st, MaxSum{s_red[0][i], s_red[1][i]}, c);
-    high = fmaxf(high, s_red[2][i]);
+    for (int i = 0; i < WAVES; ++i) m = fmaxf(m, s_red[0][i]);
+    st = MaxSum{m, 0.0f};
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) st.s += s_red[1][i] * exp2_hw((s_red[0][i] - finite_or_zero(m)) * c);
   }
-  __syncthreads();
-  const float e = exp2_hw((t - finite_or_zero(high)) * kLog2e);  // 0 for an absent entry
-  const float esum = wave_sum(e);
-  if (lane == 0) s_red[0][wave] = esum;
-  __syncthreads();
-  float total = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kDistWaves; ++i) total += s_red[0][i];
+  for (int i = 0; i < WAVES; ++i) high = fmaxf(high, s_red[2][i]);
+  // p: exponentials in place (0 for an absent entry), then their sum
+  float sum = 0.0f, part = 0.0f;
   const bool any = high > -INFINITY;
-  const float prob = any ? e / total : 0.0f;
-  if (mine) s_p[tid] = prob;
   const float w = !any ? 0.0f : p.weight ? p.weight[row] : 1.0f;
-
   const bool empty = LOSS ? st.s == 0.0f : p.lse[row] == -INFINITY;  // every logit is -inf
   const float ref = finite_or_zero(st.m);
   const float l2s = empty ? 0.0f : __builtin_amdgcn_logf(st.s);
+  for (int j = tid; j < p.K; j += TH) {
+    const float t = s_p[j], e = exp2_hw((t - finite_or_zero(high)) * kLog2e);
+    if (LOSS && e > 0.0f) {  // e (log e - log q): the loss is this sum over the e's sum, less its logarithm
+      const float logq = empty ? -INFINITY : (s_z[j] - ref) / p.temperature - l2s * kLn2;
+      part += e * ((t - high) - logq);
+    }
+    s_p[j] = e;
+    sum += e;
+  }
+  sum = block_sum<WAVES>(sum, s_red[0]);
   if (LOSS) {
-    const float lse = empty ? -INFINITY : ref / p.temperature + l2s * kLn2;
-    const float logq = empty ? -INFINITY : (z - ref) / p.temperature - l2s * kLn2;
-    const float logp = (t - high) - __logf(total);
-    const float term = wave_sum(prob > 0.0f && w != 0.0f ? prob * (logp - logq) : 0.0f);
-    if (lane == 0) s_red[1][wave] = term;
-    __syncthreads();
+    part = block_sum<WAVES>(part, s_red[1]);
     if (tid == 0) {
-      float l = 0.0f;
-      for (int i = 0; i < kDistWaves; ++i) l += s_red[1][i];
-      p.loss[row] = w == 0.0f ? 0.0f : l * w;
-      p.lse[row] = lse;
+      p.loss[row] = w == 0.0f ? 0.0f : (part / sum - __logf(sum)) * w;
+      p.lse[row] = empty ? -INFINITY : ref / p.temperature + l2s * kLn2;
     }
   }
   if (!GRAD) return;
 
   // q of a logit: from the pass above, or from the given lse
+  const float wt = w / p.temperature, norm = any ? 1.0f / sum : 0.0f;
   const float lse_in = LOSS || empty ? 0.0f : p.lse[row], inv_tau = 1.0f / p.temperature;
-  auto q = [&](float v) {
-    return LOSS ? exp2_hw(__builtin_fmaf(v - ref, c, -l2s)) : exp2_hw(__builtin_fmaf(v, inv_tau, -lse_in) * kLog2e);
+  const Exp eq{ref, c, -l2s};
+  const auto q = [&](float v) {
+    return LOSS ? eq(v) : exp2_hw(__builtin_fmaf(v, inv_tau, -lse_in) * kLog2e);
   };
-  const float wt = w / p.temperature;
   char* g = static_cast<char*>(p.grad) + row * p.V * (BF16 ? 2 : 4);
-  for (int64_t v = tid; v < nvec; v += kDistThreads) {
-    u32x4 o = {0u, 0u, 0u, 0u};
-    if (w != 0.0f) {
-      const u32x4 d = dist_load<BF16>(x, v);
-      float e2[N];
+  const auto put = [&](int64_t v, const u32x4& d) {
+    float e[N];
 #pragma unroll
-      for (int k = 0; k < N; ++k) e2[k] = q(dist_elem<BF16>(d, k)) * wt;
+    for (int k = 0; k < N; ++k) e[k] = q(dist_elem<BF16>(d, k)) * wt;
+    u32x4 o;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        o[k] = BF16 ? bf16_rne(e2[(2 * k) % N]) | (bf16_rne(e2[(2 * k + 1) % N]) << 16) : __float_as_uint(e2[k]);
-    }
+    for (int k = 0; k < 4; ++k) o[k] = BF16 ? bf16_pair(e[(2 * k) % N], e[(2 * k + 1) % N]) : __float_as_uint(e[k]);
     *reinterpret_cast<typename Vec16<BF16>::raw*>(g + 16 * v) = o;
+  };
+  if (w == 0.0f) {  // uniform: whatever the logits hold
+    for (int64_t v = tid; v < nvec; v += TH)
+      *reinterpret_cast<typename Vec16<BF16>::raw*>(g + 16 * v) = u32x4{0u, 0u, 0u, 0u};
+    if (tail) dist_put<BF16>(g, nvec * N + tid, 0.0f);
+    return;
   }
-  if (nvec * N + tid < p.V)
-    dist_put<BF16>(g, nvec * N + tid, w != 0.0f ? q(dist_at<BF16>(x, nvec * N + tid)) * wt : 0.0f);
+  if (HOLD > 0) {
+#pragma unroll
+    for (int k = 0; k < HOLD; ++k) {
+      if (tid + k * TH < nvec) put(tid + k * TH, held[k]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+    int64_t v = tid;
+    for (; v + 3 * TH < nvec; v += 4 * TH) {
+      u32x4 d[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) d[k] = dist_load<BF16>(x, v + k * TH);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) put(v + k * TH, d[k]);
+    }
+    for (; v < nvec; v += TH) put(v, dist_load<BF16>(x, v));
+  }
+  if (tail) dist_put<BF16>(g, nvec * N + tid, q(last) * wt);
   __syncthreads();  // the dense gradient is written: correct the teacher's entries
-  if (at >= 0 && w != 0.0f) {
+  for (int j = tid; j < p.K; j += TH) {
+    const int32_t at = s_idx[j];
+    if (at < 0) continue;
     float target = 0.0f;  // an index named twice takes the sum, in the entries' order, from each of its threads
-    for (int j = 0; j < p.K; ++j)
-      if (s_idx[j] == at) target += s_p[j];
-    dist_put<BF16>(g, at, (q(z) - target) * wt);
+    for (int i = 0; i < p.K; ++i)
+      if (s_idx[i] == at) target += s_p[i];
+    dist_put<BF16>(g, at, (q(s_z[j]) - target * norm) * wt);
   }
+}
+
+template <bool BF16, int TH, int HOLD, bool LOSS, bool GRAD>
+static void launch_distill_as(const DistillArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((k_distill<BF16, TH, HOLD, LOSS, GRAD>), dim3((unsigned)a.T), dim3(TH), 0, st, a);
 }
 
 template <bool BF16>
-static void launch_distill_t(const DistillArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)a.T), block(kDistThreads);
-  if (!a.grad)
-    hipLaunchKernelGGL((k_distill<BF16, true, false>), grid, block, 0, st, a);
-  else if (a.loss)
-    hipLaunchKernelGGL((k_distill<BF16, true, true>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((k_distill<BF16, false, true>), grid, block, 0, st, a);
+static void launch_distill_t(const DistillArgs& a, int cus, hipStream_t st) {
+  const int64_t vecs = a.V / Vec16<BF16>::kN;
+  const bool few = a.T < 2 * cus;  // then a row's own time counts: 1024 threads
+  if (a.grad && a.loss) {
+    if (vecs <= 256 * 4)
+      launch_distill_as<BF16, 256, 4, true, true>(a, st);
+    else if (vecs <= 256 * 16 && !few)
+      launch_distill_as<BF16, 256, 16, true, true>(a, st);
+    else if (vecs <= 1024 * 8)
+      launch_distill_as<BF16, 1024, 8, true, true>(a, st);
+    else if (vecs <= 1024 * 16)
+      launch_distill_as<BF16, 1024, 16, true, true>(a, st);
+    else
+      launch_distill_as<BF16, 1024, 0, true, true>(a, st);
+  } else if (a.loss) {
+    if (vecs <= 256 * 8 && !few)
+      launch_distill_as<BF16, 256, 0, true, false>(a, st);
+    else if (!few)
+      launch_distill_as<BF16, 512, 0, true, false>(a, st);
+    else
+      launch_distill_as<BF16, 1024, 0, true, false>(a, st);
+  } else {
+    if (vecs <= 256 * 8 && !few)
+      launch_distill_as<BF16, 256, 0, false, true>(a, st);
+    else
+      launch_distill_as<BF16, 1024, 0, false, true>(a, st);
+  }
 }
 
-void launch_distill(const DistillArgs& a, hipStream_t st) {
+void launch_distill(const DistillArgs& a, int cus, hipStream_t st) {
   if (a.bf16)
-    launch_distill_t<true>(a, st);
+    launch_distill_t<true>(a, cus, st);
   else
-    launch_distill_t<false>(a, st);
+    launch_distill_t<false>(a, cus, st);
 }
 
 }  // namespace nvfp4

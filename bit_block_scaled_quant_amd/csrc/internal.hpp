@@ -100,7 +100,7 @@ struct DistillArgs {
 
 constexpr int kDistillMaxK = 1024;
 
-void launch_distill(const DistillArgs& a, hipStream_t st);
+void launch_distill(const DistillArgs& a, int cus, hipStream_t st);
 
 // Embedding lookup and the gradient of its table
 struct EmbedArgs {
