@@ -388,145 +388,194 @@ __global__ __launch_bounds__(kGemmThreads, MT == 4 ? 1 : 2) void k_ffn_m32(FfnAr
 }
 
 // ---- few tokens: the weights are read once ----------------------------------
-// Up to 64 rows of X.  A workgroup owns 16 columns (16 gate and 16 up rows of
-// W, one MFMA tile each) and all of K; its four waves take every fourth chunk
-// of 256 K-elements, straight from memory into registers, the next chunk's
-// loads in flight while the present one multiplies, and join their sums in LDS
-// in the order of the waves.  Lane l of a wave reads row l % 16 of each 16-row
-// tile and the 64 K-elements 64 (l / 16) .. of a chunk: 32 bytes of codes and
-// four scale bytes, which feed eight MFMA slices (X and W use the same map, so
-// the products pair up).  K % 64 == 0: past its end both scales are zero.
-// At F = 10240, K = 5120 one token takes 18.5 us and 45 take 35 (the weights are
-// 59 MB, 12 us of memory time; past 16 tokens the unpack of X, once for every
-// 16 columns, adds about 7 us for each 16 tokens).  32 columns a workgroup take
-// 24 and 36 us (too few workgroups to spread evenly), eight waves 18 and 41.
-constexpr int kSkinnyThreads = 256, kSkinnyWaves = kSkinnyThreads / 64;
+// Up to 64 rows of X a workgroup.  A 16-row MFMA tile of W takes 8 gate rows
+// and the up rows of the same 8 columns, so the chip's columns are dealt out in
+// eights: a workgroup owns TW tiles (8 TW columns) and all of K.  Its eight
+// waves take turns at the chunks of 128 H elements, straight from memory into
+// registers, BUFS - 1 chunks in flight while one multiplies, and join their sums
+// in LDS in a fixed order.  Lane l of a wave reads row l % 16 of each tile and
+// the 32 H K-elements 32 H (l / 16) .. of a chunk: 16 H bytes of codes and 2 H
+// scale bytes, which feed 4 H MFMA slices (X and W use the same map, so the
+// products pair up).  K % 64 == 0: past its end both scales are zero.
+//
+// TW is the share of a CU, so that one round of workgroups covers F and X is
+// unpacked once a CU.  At F = 10240, K = 5120 (the weights are 59 MB, 11.5 us at
+// a large copy's rate) one token takes 16 us and 45 take 22; 16 columns for each
+// of 640 workgroups took 16 and 32.5.  The loads alone take 12.5 and 17.6 us; the
+// unpack of the last chunks, when nothing is left to load, is the rest.  Chunks
+// of whole 128-byte lines (H = 2) beat halves where the registers hold them (45
+// tokens: 22 us against 25.6); loads past the caches lose (one token: 16.9).
+constexpr int kSkinnyThreads = 512, kSkinnyWaves = kSkinnyThreads / 64;
 
-template <int T>
+template <int T, int H>
 struct SkinnyRows {
-  uint4 q[T][2];
+  uint4 q[T][H];
   uint32_t sc[T];
 };
 
-template <int T>
-__device__ __forceinline__ void skinny_load(const uint8_t* (&codes)[T], const uint8_t* (&scales)[T], int64_t c,
-                                            bool in, SkinnyRows<T>& d) {
-  const int64_t co = in ? c * 128 : 0, so = in ? c * 16 : 0;  // (past the end: the row's start, unused)
+// codes and scales at the rows' offsets, which fit 32 bits
+template <int T, int H>
+__device__ __forceinline__ void skinny_load(const uint8_t* codes, const uint8_t* scales, const uint32_t (&row)[T],
+                                            uint32_t kb, uint32_t at, bool in, SkinnyRows<T, H>& d) {
 #pragma unroll
   for (int t = 0; t < T; ++t) {
-    d.q[t][0] = *reinterpret_cast<const uint4*>(codes[t] + co);
-    d.q[t][1] = *reinterpret_cast<const uint4*>(codes[t] + co + 16);
-    const uint32_t s = *reinterpret_cast<const uint32_t*>(scales[t] + so);
+    const uint32_t off = row[t] * kb + at;
+#pragma unroll
+    for (int h = 0; h < H; ++h) d.q[t][h] = *reinterpret_cast<const uint4*>(codes + (off + 16 * h));
+    const uint8_t* sp = scales + off / 8;
+    const uint32_t s = H == 2 ? *reinterpret_cast<const uint32_t*>(sp) : *reinterpret_cast<const uint16_t*>(sp);
     d.sc[t] = in ? s : 0u;
   }
 }
 
-template <int MT, bool GRAD>
-__global__ __launch_bounds__(kSkinnyThreads, 2) void k_ffn_skinny(FfnArgs p) {
-  constexpr int TW = 2;  // a tile of gate rows, a tile of up rows
-  __shared__ __align__(16) float s_acc[kSkinnyWaves][MT * TW][64][4];
+template <int MT, int TW, bool GRAD>
+__global__ __launch_bounds__(kSkinnyThreads, 1) void k_ffn_skinny(FfnArgs p) {
+  // what a lane's 256 registers hold beside the sums: three whole lines of every
+  // row, two, or halves of lines
+  constexpr int kRows = MT + TW, kSums = 4 * MT * TW;
+  constexpr int H = 18 * kRows + kSums <= 210 ? 2 : 1;
+  constexpr int BUFS = (H == 2 ? 27 : 15) * kRows + kSums <= 200 ? 3 : 2;
+  __shared__ __align__(16) float s_acc[kSkinnyWaves / 2][MT * TW][64][4];
   const GemmArgs& g = p.g;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, kb = g.K / 2, ks = g.K / 16;
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * (8 * TW);
+  const uint32_t K = (uint32_t)g.K, kb = K / 2;
   const float ts_a = g.a_ts[0], ts_b = g.b_ts[0];
-  // the lane's 64 elements of the first chunk; where K is shorter than that,
-  // the first lanes' ones stand in
-  const int part = 64 * lg < g.K ? lg : 0;
-  const uint8_t *wc[TW], *ws[TW], *xc[MT], *xs[MT];
+  uint32_t wr[TW], xr[MT];
 #pragma unroll
-  for (int t = 0; t < TW; ++t) {
-    const int64_t row = min(n0 + li, p.F - 1) + t * p.F;
-    wc[t] = g.b_codes + row * kb + 32 * part;
-    ws[t] = g.b_scales + row * ks + 4 * part;
-  }
+  for (int t = 0; t < TW; ++t) wr[t] = (uint32_t)(min(n0 + 8 * t + (li & 7), p.F - 1) + (li >> 3) * p.F);
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t row = min<int64_t>(i * 16 + li, g.M - 1);
-    xc[i] = g.a_codes + row * kb + 32 * part;
-    xs[i] = g.a_scales + row * ks + 4 * part;
-  }
+  for (int i = 0; i < MT; ++i) xr[i] = (uint32_t)min<int64_t>(i * 16 + li, g.M - 1);
   floatx4 acc[MT][TW];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int t = 0; t < TW; ++t) acc[i][t] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  const int64_t nc = (g.K + 255) / 256;
-  SkinnyRows<TW> w0, w1;
-  SkinnyRows<MT> x0, x1;
-  auto load = [&](int64_t c, SkinnyRows<TW>& w, SkinnyRows<MT>& x) {
-    const bool in = c * 256 + 64 * lg < g.K;
-    skinny_load<TW>(wc, ws, c, in, w);
-    skinny_load<MT>(xc, xs, c, in, x);
+  const int nc = (int)((K + 128 * H - 1) / (128 * H));
+  SkinnyRows<TW, H> w[BUFS];
+  SkinnyRows<MT, H> x[BUFS];
+  auto load = [&](int c, SkinnyRows<TW, H>& wd, SkinnyRows<MT, H>& xd) {
+    const uint32_t k = c * (128 * H) + 32 * H * lg;
+    const bool in = k < K;  // else the row's start stands in
+    skinny_load<TW, H>(g.b_codes, g.b_scales, wr, kb, in ? k / 2 : 0u, in, wd);
+    skinny_load<MT, H>(g.a_codes, g.a_scales, xr, kb, in ? k / 2 : 0u, in, xd);
   };
-  auto multiply = [&](const SkinnyRows<TW>& w, const SkinnyRows<MT>& x) {
+  auto multiply = [&](const SkinnyRows<TW, H>& wd, const SkinnyRows<MT, H>& xd) {
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      half8 fw[TW], fx[MT];
+    for (int s = 0; s < 4 * H; ++s) {
+      half8 fx[MT];
 #pragma unroll
-      for (int t = 0; t < TW; ++t) fw[t] = unpack8(raw_word(w.q[t][s >> 2], s & 3), scale_h2(w.sc[t] >> (8 * (s >> 1))));
+      for (int i = 0; i < MT; ++i) fx[i] = unpack8(raw_word(xd.q[i][s >> 2], s & 3), scale_h2(xd.sc[i] >> (8 * (s >> 1))));
 #pragma unroll
-      for (int i = 0; i < MT; ++i) fx[i] = unpack8(raw_word(x.q[i][s >> 2], s & 3), scale_h2(x.sc[i] >> (8 * (s >> 1))));
+      for (int t = 0; t < TW; ++t) {
+        const half8 fw = unpack8(raw_word(wd.q[t][s >> 2], s & 3), scale_h2(wd.sc[t] >> (8 * (s >> 1))));
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int t = 0; t < TW; ++t) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fx[i], fw[t], acc[i][t], 0, 0, 0);
-    }
-  };
-  int64_t c = wave;
-  if (c < nc) load(c, w0, x0);
-  while (c < nc) {  // (every condition is wave-uniform)
-    if (c + kSkinnyWaves < nc) load(c + kSkinnyWaves, w1, x1);
-    multiply(w0, x0);
-    c += kSkinnyWaves;
-    if (c >= nc) break;
-    if (c + kSkinnyWaves < nc) load(c + kSkinnyWaves, w0, x0);
-    multiply(w1, x1);
-    c += kSkinnyWaves;
-  }
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int t = 0; t < TW; ++t) *reinterpret_cast<floatx4*>(s_acc[wave][i * TW + t][lane]) = acc[i][t];
-  __syncthreads();
-
-  // wave v joins and emits row tile v: lane holds rows 4 lg .. 4 lg + 3 of
-  // column li
-  const float inv_a = __fdiv_rn(1.0f, ts_a), inv_b = __fdiv_rn(1.0f, ts_b);
-  float amax = 0.0f;
-  for (int i = wave; i < MT; i += kSkinnyWaves) {
-    floatx4 v[TW];
-#pragma unroll
-    for (int t = 0; t < TW; ++t) {
-      v[t] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < kSkinnyWaves; ++s) {
-        const floatx4 d = *reinterpret_cast<const floatx4*>(s_acc[s][i * TW + t][lane]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[t][k] += d[k];
+        for (int i = 0; i < MT; ++i) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fx[i], fw, acc[i][t], 0, 0, 0);
       }
     }
-    const int64_t n = n0 + li;
+  };
+  // (every condition is wave-uniform)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t m = i * 16 + 4 * lg + k;
-      if (m >= g.M || n >= p.F) continue;
-      const float d = GRAD ? get(p, m * p.F + n) : 0.0f;
+  for (int b = 0; b < BUFS - 1; ++b)
+    if (wave + b * kSkinnyWaves < nc) load(wave + b * kSkinnyWaves, w[b], x[b]);
+  for (int c = wave; c < nc; c += BUFS * kSkinnyWaves) {
+#pragma unroll
+    for (int b = 0; b < BUFS; ++b) {
+      if (c + b * kSkinnyWaves >= nc) break;
+      const int ahead = c + (b + BUFS - 1) * kSkinnyWaves;
+      if (ahead < nc) load(ahead, w[(b + BUFS - 1) % BUFS], x[(b + BUFS - 1) % BUFS]);
+      multiply(w[b], x[b]);
+    }
+  }
+  // waves 4 .. 7 hand their sums to waves 0 .. 3, those theirs to everyone
+  constexpr int kHalf = kSkinnyWaves / 2;
+  if (wave >= kHalf) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int t = 0; t < TW; ++t) *reinterpret_cast<floatx4*>(s_acc[wave - kHalf][i * TW + t][lane]) = acc[i][t];
+  }
+  __syncthreads();
+  if (wave < kHalf) {  // (each lane reads and writes its own places)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int t = 0; t < TW; ++t) {
+        float* at = s_acc[wave][i * TW + t][lane];
+        const floatx4 o = *reinterpret_cast<const floatx4*>(at);
+        floatx4 v;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = acc[i][t][k] + o[k];
+        *reinterpret_cast<floatx4*>(at) = v;
+      }
+  }
+  __syncthreads();
+
+  // A tile's lane (li, lg) holds rows 4 lg .. 4 lg + 3 of gate column li (li <
+  // 8) or up column li - 8; the lanes of such a pair emit two rows each.
+  const float inv_a = __fdiv_rn(1.0f, ts_a), inv_b = __fdiv_rn(1.0f, ts_b);
+  float amax = 0.0f;
+  for (int v = wave; v < MT * TW; v += kSkinnyWaves) {
+    const int k0 = 2 * (li >> 3), from = lane & ~8;
+    float a[2] = {0.f, 0.f}, u[2] = {0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < kHalf; ++s) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        a[k] += s_acc[s][v][from][k0 + k];
+        u[k] += s_acc[s][v][from + 8][k0 + k];
+      }
+    }
+    const int64_t n = n0 + 8 * (v % TW) + (li & 7), m = 16 * (v / TW) + 4 * lg + k0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (m + k >= g.M || n >= p.F) continue;
+      const float d = GRAD ? get(p, (m + k) * p.F + n) : 0.0f;
       if (p.act == kSilu)
-        emit<kSilu, GRAD>(p, m, n, (v[0][k] * inv_a) * inv_b, (v[1][k] * inv_a) * inv_b, d, amax);
+        emit<kSilu, GRAD>(p, m + k, n, (a[k] * inv_a) * inv_b, (u[k] * inv_a) * inv_b, d, amax);
       else
-        emit<kGelu, GRAD>(p, m, n, (v[0][k] * inv_a) * inv_b, (v[1][k] * inv_a) * inv_b, d, amax);
+        emit<kGelu, GRAD>(p, m + k, n, (a[k] * inv_a) * inv_b, (u[k] * inv_a) * inv_b, d, amax);
     }
   }
   if (GRAD && g.amax) amax_to(g, amax);
 }
 
-template <int MT, bool GRAD>
-static void launch_skinny(const FfnArgs& p, hipStream_t st) {
-  hipLaunchKernelGGL((k_ffn_skinny<MT, GRAD>), dim3((unsigned)((p.F + 15) / 16)), dim3(kSkinnyThreads), 0, st, p);
+static int64_t tiles_of(int64_t n, int64_t size) { return (n + size - 1) / size; }
+
+template <int MT, int TW, bool GRAD>
+static void launch_skinny_as(const FfnArgs& p, hipStream_t st) {
+  hipLaunchKernelGGL((k_ffn_skinny<MT, TW, GRAD>),
+                     dim3((unsigned)tiles_of(p.F, 8 * TW)), dim3(kSkinnyThreads), 0, st, p);
 }
 
-static int64_t tiles_of(int64_t n, int64_t size) { return (n + size - 1) / size; }
+// tiles of 8 columns for each CU, up to what the registers hold beside four row
+// tiles; wider blocks take more rounds
+template <int MT, bool GRAD>
+static void launch_skinny_mt(const FfnArgs& p, int cus, hipStream_t st) {
+  const int64_t each = tiles_of(tiles_of(p.F, 8), cus);
+  if (each <= 1)
+    launch_skinny_as<MT, 1, GRAD>(p, st);
+  else if (each <= 2)
+    launch_skinny_as<MT, 2, GRAD>(p, st);
+  else if (each <= 3)
+    launch_skinny_as<MT, 3, GRAD>(p, st);
+  else if (each == 4)
+    launch_skinny_as<MT, 4, GRAD>(p, st);
+  else
+    launch_skinny_as<MT, 5, GRAD>(p, st);
+}
+
+template <bool GRAD>
+static void launch_skinny(const FfnArgs& p, int cus, hipStream_t st) {
+  switch (tiles_of(p.g.M, 16)) {
+    case 1: return launch_skinny_mt<1, GRAD>(p, cus, st);
+    case 2: return launch_skinny_mt<2, GRAD>(p, cus, st);
+    case 3: return launch_skinny_mt<3, GRAD>(p, cus, st);
+    default: return launch_skinny_mt<4, GRAD>(p, cus, st);
+  }
+}
 
 template <int NT, int MT, bool GRAD>
 static void launch_m32(const FfnArgs& p, bool whole_k, const M32Grid& gr, hipStream_t st) {
@@ -554,15 +603,8 @@ static void launch_ffn_t(const FfnArgs& p, int cus, hipStream_t st) {
   const bool stages = g.K % 64 == 0 && g.K <= (INT64_C(1) << 24) && (uintptr_t)g.a_codes % 16 == 0 &&
                       (uintptr_t)g.b_codes % 16 == 0 && (uintptr_t)g.a_scales % 4 == 0 &&
                       (uintptr_t)g.b_scales % 4 == 0;
-  if (stages && g.M <= 64) {
-    if (g.M <= 16)
-      launch_skinny<1, GRAD>(p, st);
-    else if (g.M <= 32)
-      launch_skinny<2, GRAD>(p, st);
-    else if (g.M <= 48)
-      launch_skinny<3, GRAD>(p, st);
-    else
-      launch_skinny<4, GRAD>(p, st);
+  if (stages && g.M <= 64 && p.F * g.K < (INT64_C(1) << 32)) {  // (its byte offsets are 32 bits)
+    launch_skinny<GRAD>(p, cus, st);
     return;
   }
   if (stages) {

@@ -104,6 +104,14 @@ def test_few_tokens(M, F, K, dtype):
     run(M, F, K, nv.SILU, dtype, seed=M + K)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M", [1, 20, 48, 63])
+@pytest.mark.parametrize("F,K", [(2050, 448), (4100, 1088), (6147, 320), (20501, 128), (8185, 64)])
+def test_few_tokens_column_shares(M, F, K, dtype):
+    """Each share of columns that a compute unit can have, the last one ragged."""
+    run(M, F, K, nv.GELU, dtype, seed=M + F)
+
+
 @pytest.mark.parametrize("act", [nv.SILU, nv.GELU])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("M,F,K", [(2100, 2736, 832), (4096, 2048, 1024), (4000, 2100, 704), (3900, 2303, 512),
