@@ -52,13 +52,6 @@ __device__ __forceinline__ float dist_at(const char* row, int64_t i) {
   return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
 }
 
-// two fp32 values rounded to nearest-even bf16 in one word (NaN stays NaN)
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
-}
-
 template <bool BF16>
 __device__ __forceinline__ void dist_put(char* row, int64_t i, float v) {
   if (BF16)

@@ -35,8 +35,7 @@ __global__ __launch_bounds__(kEmbThreads) void k_embed(EmbedArgs p, int lpr_log2
         const u32x4 w = *reinterpret_cast<const u32x4_a2*>(src + 16 * i);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          o[k] = BF16 ? bf16_rne(__uint_as_float(w[k] << 16) * p.scale) |
-                            (bf16_rne(__uint_as_float(w[k] & 0xFFFF0000u) * p.scale) << 16)
+          o[k] = BF16 ? bf16_pair(__uint_as_float(w[k] << 16) * p.scale, __uint_as_float(w[k] & 0xFFFF0000u) * p.scale)
                       : __float_as_uint(__uint_as_float(w[k]) * p.scale);
       }
       *reinterpret_cast<u32x4_a2*>(dst + 16 * i) = o;
@@ -44,7 +43,7 @@ __global__ __launch_bounds__(kEmbThreads) void k_embed(EmbedArgs p, int lpr_log2
     for (int64_t i = nvec * N + l; i < p.D; i += lpr) {
       if (BF16) {
         const uint32_t h = reinterpret_cast<const uint16_t*>(src)[i];
-        reinterpret_cast<uint16_t*>(dst)[i] = ok ? (uint16_t)bf16_rne(__uint_as_float(h << 16) * p.scale) : 0;
+        reinterpret_cast<uint16_t*>(dst)[i] = ok ? (uint16_t)bf16_pair(__uint_as_float(h << 16) * p.scale, 0.0f) : 0;
       } else {
         reinterpret_cast<float*>(dst)[i] = ok ? reinterpret_cast<const float*>(src)[i] * p.scale : 0.0f;
       }

@@ -24,7 +24,7 @@ constexpr float kGeluC2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 struct Sigmoid { float s, om; };  // sigma(y), 1 - sigma(y)
 
 __device__ __forceinline__ Sigmoid sigmoid(float y) {
-  const float t = __expf(-fabsf(y));
+  const float t = __builtin_amdgcn_exp2f(fabsf(y) * -1.4426950408889634f);
   const float r = __builtin_amdgcn_rcpf(1.0f + t);
   return y >= 0.0f ? Sigmoid{r, t * r} : Sigmoid{t * r, r};
 }
@@ -55,7 +55,7 @@ __device__ __forceinline__ void act_both(float a, float& h, float& slope) {
 // stores one value and returns the magnitude stored
 __device__ __forceinline__ float put(const FfnArgs& p, int64_t idx, float v) {
   if (p.bf16) {
-    const uint32_t h = bf16_rne(v);
+    const uint32_t h = bf16_pair(v, 0.0f);
     static_cast<uint16_t*>(p.out)[idx] = (uint16_t)h;
     return fabsf(__uint_as_float(h << 16));
   }
@@ -226,11 +226,12 @@ struct M32Paired {
 // Two neighbouring columns of bf16 in one word: columns n and n + 1 sit in
 // lanes r and r ^ 1, values k and k + 1 (k even) in rows m and m + 1.  The lane
 // pair swaps one value, so the even lane holds row m's pair of columns and the
-// odd lane row m + 1's.
+// odd lane row m + 1's; the swap comes before the rounding, which then takes one
+// instruction for the pair.
 __device__ __forceinline__ uint32_t pair_words(float v0, float v1, bool odd) {
-  const uint32_t h0 = bf16_rne(v0), h1 = bf16_rne(v1);
-  const uint32_t other = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? h0 : h1), 0xB1, 0xF, 0xF, true);
-  return odd ? (other | (h1 << 16)) : (h0 | (other << 16));
+  const float other = __uint_as_float(
+      (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(odd ? v0 : v1), 0xB1, 0xF, 0xF, true));
+  return bf16_pair(odd ? other : v0, odd ? v1 : other);
 }
 
 __device__ __forceinline__ float max_bf16_pair(float m, uint32_t w) {

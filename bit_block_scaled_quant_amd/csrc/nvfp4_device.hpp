@@ -402,6 +402,13 @@ __device__ __forceinline__ uint32_t bf16_rne(float v) {  // finite or inf
   return (b + 0x7FFFu + ((b >> 16) & 1u)) >> 16;
 }
 
+// two fp32 values rounded to nearest-even bf16 in one word (NaN stays NaN)
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 __device__ __forceinline__ float amax16(const float v[16]) {
   float m = 0.0f;
 #pragma unroll
