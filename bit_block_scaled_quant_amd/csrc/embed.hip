@@ -52,18 +52,23 @@ __global__ __launch_bounds__(kEmbThreads) void k_embed(EmbedArgs p, int lpr_log2
 }
 
 // ---- gradient of the table ------------------------------------------------
-// 1. k_embed_sort: each workgroup sorts 8192 tokens by row, stably, in LDS.
-//    Past 8192 tokens, k_embed_merge merges pairs of sorted runs, each entry
-//    finding its place by a binary search, once for each doubling.
-// 2. k_embed_fill writes zeros everywhere, which bounds a training batch (2.7
+// 1. k_embed_fill writes zeros everywhere, which bounds a training batch (2.7
 //    GB for [131072][5120]).  The store must wait for nothing and be the only
 //    one of its thread: 390 us for one 16-byte store a thread in workgroups of
 //    256, 435 for two, 470 for eight, 550 for a grid-stride loop, and 555 when
 //    each thread also looks up whether its row has tokens (measured; with that
 //    the rows below would not be written twice, 3% of the bytes).
-// 3. k_embed_few: the lanes at an entry that begins a row sum the row if it has
-//    at most kFew entries, and list it otherwise.
-// 4. k_embed_many sums the listed rows, a workgroup per 256 columns.
+// 2. k_embed_sort: each workgroup sorts 8192 tokens by row, stably, in LDS (24
+//    us; as the first workgroups of the fill it is hidden, but the fill then
+//    needs the sort's large workgroups and takes 25 us more).  Past 8192 tokens,
+//    k_embed_merge merges pairs of sorted runs, each entry finding its place by a
+//    binary search, once for each doubling.
+// 3. k_embed_sums: the lanes at an entry that begins a row sum the row if it has
+//    at most kFew entries; rows with more are summed from a list by workgroups of
+//    64 columns.  A lone run's sort leaves the list, so that both kinds go in one
+//    launch (76 us, 93 one after the other; 104 with 256 columns, since the
+//    longest row then decides); else the lanes of the first kind list those rows
+//    for a second launch.
 // Every sum has one order: that of the positions, cut into equal parts for the
 // groups that share a row.
 //
@@ -73,7 +78,6 @@ __global__ __launch_bounds__(kEmbThreads) void k_embed(EmbedArgs p, int lpr_log2
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kRun = 8192, kPer = kRun / kSortThreads;  // entries a run, at most a thread
 constexpr int kFew = 8;
-constexpr int kManyThreads = 1024;
 
 // four columns of a row, as loaded
 template <bool BF16>
@@ -145,6 +149,9 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_sort(EmbedArgs p, int bi
   __shared__ uint32_t s_key[kRun];
   __shared__ uint16_t s_pos[kRun];
   __shared__ int s_at[kSortWaves][64];  // a wave's entries of each digit, then where they go
+  __shared__ uint32_t s_many;           // rows listed
+  __shared__ uint16_t s_first[kRun / (kFew + 1)];
+  static_assert(kRun / (kFew + 1) <= kSortThreads, "a thread for each listed row");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t t0 = (int64_t)blockIdx.x * kRun;
   // a lone run needs no more rounds than its tokens fill; others are merged whole
@@ -160,7 +167,8 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_sort(EmbedArgs p, int bi
     const uint32_t tok = t < p.T ? (uint32_t)p.tok[t] : ~0u;
     key[k] = tok < (uint32_t)p.V ? tok : (uint32_t)p.V;
   }
-  if (blockIdx.x == 0 && tid == 0) *p.count = 0u;
+  if (tid == 0) s_many = 0u;
+  if (gridDim.x > 1 && blockIdx.x == 0 && tid == 0) *p.count = 0u;
   for (int shift = 0; shift < bits; shift += 6) {
     s_at[wave][lane] = 0;
     __builtin_amdgcn_wave_barrier();
@@ -216,6 +224,41 @@ __global__ __launch_bounds__(kSortThreads) void k_embed_sort(EmbedArgs p, int bi
     const int at = mine + 64 * k;
     p.sorted[t0 + at] = make_uint2(key[k], (uint32_t)(t0 + pos[k]));
   }
+  if (gridDim.x > 1) return;
+  // the rows with more than kFew entries (s_key is sorted; padding has key V):
+  // where they begin, in any order, then, a thread each, where they end
+  const int n = per * kSortThreads;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (k >= per) break;
+    const int at = mine + 64 * k;
+    const uint32_t row = key[k];
+    if (row < p.V && at + kFew < n && s_key[at + kFew] == row && (at == 0 || s_key[at - 1] != row))
+      s_first[atomicAdd(&s_many, 1u)] = (uint16_t)at;
+  }
+  __syncthreads();
+  if (tid == 0) *p.count = s_many;
+  if (tid >= (int)s_many) return;
+  const int first = s_first[tid];
+  const uint32_t row = s_key[first];
+  int lo = first + kFew + 1, hi = n;
+  while (lo < hi) {
+    const int m = (lo + hi) / 2;
+    if (s_key[m] == row)
+      lo = m + 1;
+    else
+      hi = m;
+  }
+  p.many[tid] = make_uint2((uint32_t)first, (uint32_t)(lo - first));
+}
+
+__global__ __launch_bounds__(kEmbThreads) void k_embed_fill(float* out, int64_t n) {
+  const int64_t i = ((int64_t)blockIdx.x * kEmbThreads + threadIdx.x) * 4;
+  if (i + 4 <= n) {
+    *reinterpret_cast<f32x4_a4*>(out + i) = f32x4_a4{0.f, 0.f, 0.f, 0.f};
+  } else {
+    for (int64_t e = i; e < n; ++e) out[e] = 0.0f;
+  }
 }
 
 // Runs of `len` sorted entries of src, merged in pairs into dst: an entry of
@@ -240,22 +283,13 @@ __global__ __launch_bounds__(kEmbThreads) void k_embed_merge(const uint2* __rest
   dst[i + (lo - other) - (left ? 0 : mid - pair)] = e;
 }
 
-__global__ __launch_bounds__(kEmbThreads) void k_embed_fill(float* out, int64_t n) {
-  const int64_t i = ((int64_t)blockIdx.x * kEmbThreads + threadIdx.x) * 4;
-  if (i + 4 <= n) {
-    *reinterpret_cast<f32x4_a4*>(out + i) = f32x4_a4{0.f, 0.f, 0.f, 0.f};
-  } else {
-    for (int64_t e = i; e < n; ++e) out[e] = 0.0f;
-  }
-}
-
 // 2^lpr_log2 lanes an entry, kWide vectors of four columns a lane, two entries
 // of the row in flight
+constexpr int kWide = 4;
 template <bool BF16>
-__global__ __launch_bounds__(kEmbThreads) void k_embed_few(EmbedArgs p, int lpr_log2) {
-  constexpr int kWide = 4;
+__device__ __forceinline__ void sum_few(const EmbedArgs& p, int lpr_log2, int64_t block, int64_t part, bool list) {
   const int lpr = 1 << lpr_log2, l = threadIdx.x & (lpr - 1);
-  const int64_t i = ((int64_t)blockIdx.x * kEmbThreads + threadIdx.x) >> lpr_log2;
+  const int64_t i = (block * kEmbThreads + threadIdx.x) >> lpr_log2;
   if (i >= p.T) return;
   // entries i - 1 .. i + kFew, all at once
   const uint32_t before = i > 0 ? p.sorted[i - 1].x : ~0u;
@@ -265,7 +299,7 @@ __global__ __launch_bounds__(kEmbThreads) void k_embed_few(EmbedArgs p, int lpr_
   const uint32_t row = e[0].x;
   if (row >= p.V || before == row) return;
   if (e[kFew].x == row) {
-    if (l == 0 && blockIdx.y == 0) {  // the row's end, by bisection
+    if (list && l == 0 && part == 0) {  // the row's end, by bisection
       int64_t lo = i + kFew + 1, hi = p.T;
       while (lo < hi) {
         const int64_t m = (lo + hi) / 2;
@@ -278,7 +312,7 @@ __global__ __launch_bounds__(kEmbThreads) void k_embed_few(EmbedArgs p, int lpr_
     }
     return;
   }
-  const int64_t c0 = (int64_t)blockIdx.y * 4 * kWide * lpr + 4 * l;
+  const int64_t c0 = part * 4 * kWide * lpr + 4 * l;
   float acc[kWide][4] = {};
 #pragma unroll
   for (int q = 0; q < kFew; q += 2) {
@@ -312,13 +346,13 @@ __global__ __launch_bounds__(kEmbThreads) void k_embed_few(EmbedArgs p, int lpr_
 // One listed row and 4 * 2^lpr_log2 columns a workgroup at a time: each group
 // of lanes sums its part of the row's entries, the first joins the parts.
 template <bool BF16>
-__global__ __launch_bounds__(kManyThreads) void k_embed_many(EmbedArgs p, int lpr_log2, uint32_t chunks) {
+__device__ __forceinline__ void sum_many(const EmbedArgs& p, int lpr_log2, uint32_t chunks, uint32_t block,
+                                         uint32_t blocks, float* s_sum) {
   constexpr int kAhead = 8;  // rows of dout in flight per lane
-  __shared__ __align__(16) float s_sum[kManyThreads * 4];
   const int tid = threadIdx.x, lpr = 1 << lpr_log2;
-  const int group = tid >> lpr_log2, groups = kManyThreads >> lpr_log2;
+  const int group = tid >> lpr_log2, groups = kEmbThreads >> lpr_log2;
   const uint64_t tasks = (uint64_t)*p.count * chunks;
-  for (uint64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+  for (uint64_t task = block; task < tasks; task += blocks) {
     const uint2 listed = p.many[task / chunks];
     const int64_t i = listed.x, n = listed.y;
     const int64_t col = ((int64_t)(task % chunks) * lpr + (tid & (lpr - 1))) * 4;
@@ -352,6 +386,24 @@ __global__ __launch_bounds__(kManyThreads) void k_embed_many(EmbedArgs p, int lp
   }
 }
 
+// How the sums' workgroups are dealt out: `many` of the first row of the grid
+// take the listed rows, the others of each row one part of the columns for the
+// short rows.
+struct SumGrid {
+  uint32_t many, chunks;
+  int many_log2, few_log2;  // lanes over columns
+  bool list;                // the short rows' lanes list the long ones
+};
+
+template <bool BF16>
+__global__ __launch_bounds__(kEmbThreads) void k_embed_sums(EmbedArgs p, SumGrid g) {
+  __shared__ __align__(16) float s_sum[kEmbThreads * 4];
+  if (blockIdx.x >= g.many)
+    sum_few<BF16>(p, g.few_log2, blockIdx.x - g.many, blockIdx.y, g.list);
+  else if (blockIdx.y == 0)
+    sum_many<BF16>(p, g.many_log2, g.chunks, blockIdx.x, g.many, s_sum);
+}
+
 // ------------------------------------------------------------ launch -----
 static int log2_up(int64_t v, int lo, int hi) {
   int l = lo;
@@ -379,41 +431,44 @@ int64_t embed_grad_workspace(int64_t T) {
 }
 
 template <bool BF16>
-static void launch_embed_sums(const EmbedArgs& a, int cus, hipStream_t st) {
+static void launch_embed_sums(const EmbedArgs& a, bool listed, int cus, hipStream_t st) {
   const int64_t vecs = (a.D + 3) / 4;
-  const int lpr = log2_up((vecs + 3) / 4, 2, 6);  // lanes that cover a row at once, up to a wave
-  const int64_t per = kEmbThreads >> lpr, parts = (vecs + (4 << lpr) - 1) / (4 << lpr);
-  hipLaunchKernelGGL(k_embed_few<BF16>, dim3((unsigned)((a.T + per - 1) / per), (unsigned)parts), dim3(kEmbThreads), 0,
-                     st, a, lpr);
-  if (a.T <= kFew) return;
-  const int lm = log2_up(vecs, 4, 6);
+  const int lpr = log2_up((vecs + kWide - 1) / kWide, 2, 6);  // lanes that cover a row at once, up to a wave
+  const int64_t per = kEmbThreads >> lpr, parts = (vecs + (kWide << lpr) - 1) / (kWide << lpr);
+  const int lm = log2_up(vecs, 2, 4);
   const int64_t chunks = (vecs + (1 << lm) - 1) >> lm;
-  hipLaunchKernelGGL(k_embed_many<BF16>, dim3((unsigned)std::min<int64_t>(a.T / kFew * chunks, 2 * cus)), dim3(kManyThreads), 0, st, a, lm,
-                     (uint32_t)chunks);
+  const uint32_t many = a.T > kFew ? (uint32_t)std::min<int64_t>(a.T / kFew * chunks, 8 * cus) : 0;
+  SumGrid g{listed ? many : 0, (uint32_t)chunks, lm, lpr, !listed};
+  const dim3 grid((unsigned)(g.many + (a.T + per - 1) / per), (unsigned)parts);
+  hipLaunchKernelGGL(k_embed_sums<BF16>, grid, dim3(kEmbThreads), 0, st, a, g);
+  if (listed || many == 0) return;
+  g.many = many;
+  hipLaunchKernelGGL(k_embed_sums<BF16>, dim3(many), dim3(kEmbThreads), 0, st, a, g);
 }
 
 void launch_embed_grad(const EmbedArgs& args, void* workspace, int cus, hipStream_t st) {
   EmbedArgs a = args;
   const int64_t n = sorted_entries(a.T), vecs = (a.V * a.D + 3) / 4;
-  hipLaunchKernelGGL(k_embed_fill, dim3((unsigned)((vecs + kEmbThreads - 1) / kEmbThreads)), dim3(kEmbThreads), 0, st,
-                     static_cast<float*>(a.out), a.V * a.D);
-  if (a.T == 0) return;
+  const int runs = (int)(n / kRun);
   a.sorted = static_cast<uint2*>(workspace);
   uint2* other = a.sorted + n;
   a.many = a.sorted + (n > kRun ? 2 * n : n);
   a.count = reinterpret_cast<uint32_t*>(a.many + a.T / kFew + 1);
   int bits = 1;
   while (a.V >> bits) ++bits;  // keys 0 .. V
-  hipLaunchKernelGGL(k_embed_sort, dim3((unsigned)(n / kRun)), dim3(kSortThreads), 0, st, a, bits);
+  hipLaunchKernelGGL(k_embed_fill, dim3((unsigned)((vecs + kEmbThreads - 1) / kEmbThreads)), dim3(kEmbThreads), 0, st,
+                     static_cast<float*>(a.out), a.V * a.D);
+  if (a.T == 0) return;
+  hipLaunchKernelGGL(k_embed_sort, dim3((unsigned)runs), dim3(kSortThreads), 0, st, a, bits);
   for (int64_t len = kRun; len < n; len *= 2) {
     hipLaunchKernelGGL(k_embed_merge, dim3((unsigned)(n / kEmbThreads)), dim3(kEmbThreads), 0, st, a.sorted, other, n,
                        len);
     std::swap(a.sorted, other);
   }
   if (a.bf16)
-    launch_embed_sums<true>(a, cus, st);
+    launch_embed_sums<true>(a, runs == 1, cus, st);
   else
-    launch_embed_sums<false>(a, cus, st);
+    launch_embed_sums<false>(a, runs == 1, cus, st);
 }
 
 }  // namespace nvfp4

@@ -596,6 +596,41 @@ static void launch_m32_all(const FfnArgs& p, bool whole_k, hipStream_t st) {
   launch_m32<NT, MT, GRAD>(p, whole_k, M32Grid{rows, cols, 0, rows * cols, 1, 1}, st);
 }
 
+// Which tiles a product takes.  A CU's time for one tile is about a fixed part
+// (the first stage's load, the epilogue) and a part for each stage of 256
+// K-elements, and a launch lasts as long as the CU with the most tiles.  Fitted
+// to 64 .. 1536 tiles of K = 512 .. 5120, us a tile:
+//   forward   64 x 64: 0.75 + 1.5 a stage    128 x 64: 2.0 + 2.0   256 x 64: 5.6 + 3.7   256 x 128: 10 + 6.1
+//   gradient           2.2 + 1.5                       5.0 + 2.0             13 + 3.5               26 + 5.9
+// (256 x 128 tiles multiply fastest, 1.28 PFLOP/s against 1.08 for 128 x 64.)
+// The smaller two go two to a CU; one alone takes 1.2 of its share.  The last:
+// whole rounds of the CUs as 256 x 128 tiles, what is left as 128 x 64 in a
+// second launch (M = 1024, F = 10240, K = 5120: 190 us; 240 in whole tiles, 202
+// in small ones).
+enum Tiles { kTile64x64, kTile128x64, kTile256x64, kTile256x128, kTileMixed };
+
+static Tiles choose_tiles(int64_t M, int64_t F, int64_t K, bool grad, int cus) {
+  static const struct { int bm, bn; float fixed[2], stage[2]; } kCost[4] = {{64, 64, {0.75f, 2.2f}, {1.5f, 1.5f}},
+                                                                           {128, 64, {2.0f, 5.0f}, {2.0f, 2.0f}},
+                                                                           {256, 64, {5.6f, 13.0f}, {3.7f, 3.5f}},
+                                                                           {256, 128, {10.0f, 26.0f}, {6.1f, 5.9f}}};
+  const float stages = (float)tiles_of(K, kDirBK);
+  const auto rounds = [&](int t, int64_t tiles) {
+    const float each = (float)tiles_of(tiles, cus);
+    return (t < 2 && each == 1.0f ? 1.2f : each) * (kCost[t].fixed[grad] + kCost[t].stage[grad] * stages);
+  };
+  int best = 0;
+  float least = 0.0f;
+  for (int t = 0; t < 4; ++t) {
+    const float us = rounds(t, tiles_of(M, kCost[t].bm) * tiles_of(F, kCost[t].bn));
+    if (t == 0 || us < least) best = t, least = us;
+  }
+  const int64_t all = tiles_of(M, 256) * tiles_of(F, 128), left = all % cus;
+  constexpr float kSecondLaunch = 4.0f;
+  if (all > cus && left && rounds(3, all - left) + rounds(1, 4 * left) + kSecondLaunch < least) best = kTileMixed;
+  return (Tiles)best;
+}
+
 template <bool GRAD>
 static void launch_ffn_t(const FfnArgs& p, int cus, hipStream_t st) {
   const GemmArgs& g = p.g;
@@ -611,23 +646,16 @@ static void launch_ffn_t(const FfnArgs& p, int cus, hipStream_t st) {
   if (stages) {
     const bool whole_k =
         g.K % (2 * kDirBK) == 0 && (uintptr_t)g.a_scales % 16 == 0 && (uintptr_t)g.b_scales % 16 == 0;
-    // 256 x 128 tiles multiply fastest (1.28 PFLOP/s against 1.08 for 128 x 64,
-    // two workgroups a CU, and 0.83 for 64 x 64), but a CU without a tile, or
-    // with one more than the others, costs a whole tile's time.  So they take
-    // whole rounds of the CUs, and what is left if it fills more than half of
-    // them; else it goes as 128 x 64, which two a CU finish in 0.6 of a
-    // tile's time (M = 1024, F = 10240: 245 us in whole tiles, 220 in small
-    // ones).  Where 64 x 64 tiles do not outnumber the CUs, each CU's share is
-    // smallest with those (M = F = K = 1024: 10.7 us against 13.2 and 30.8).
-    const int64_t rows = tiles_of(g.M, 256), cols = tiles_of(p.F, 128), all = rows * cols;
-    if (tiles_of(g.M, 64) * tiles_of(p.F, 64) <= cus) {
-      launch_m32_all<2, 1, GRAD>(p, whole_k, st);
-    } else if (2 * all <= cus) {
-      launch_m32_all<2, 2, GRAD>(p, whole_k, st);
-    } else {
-      const int64_t left = all % cus, big = 2 * left > cus ? all : all - left;
-      launch_m32<4, 4, GRAD>(p, whole_k, M32Grid{rows, cols, 0, big, 1, 1}, st);
-      if (big < all) launch_m32<2, 2, GRAD>(p, whole_k, M32Grid{rows, cols, big, all - big, 2, 2}, st);
+    switch (choose_tiles(g.M, p.F, g.K, GRAD, cus)) {
+      case kTile64x64: launch_m32_all<2, 1, GRAD>(p, whole_k, st); break;
+      case kTile128x64: launch_m32_all<2, 2, GRAD>(p, whole_k, st); break;
+      case kTile256x64: launch_m32_all<2, 4, GRAD>(p, whole_k, st); break;
+      case kTile256x128: launch_m32_all<4, 4, GRAD>(p, whole_k, st); break;
+      case kTileMixed: {
+        const int64_t rows = tiles_of(g.M, 256), cols = tiles_of(p.F, 128), all = rows * cols, big = all - all % cus;
+        launch_m32<4, 4, GRAD>(p, whole_k, M32Grid{rows, cols, 0, big, 1, 1}, st);
+        launch_m32<2, 2, GRAD>(p, whole_k, M32Grid{rows, cols, big, all - big, 2, 2}, st);
+      }
     }
     return;
   }

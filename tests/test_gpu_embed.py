@@ -69,6 +69,17 @@ def test_gradient_of_many_rows_in_one_workgroup():  # every row of a range named
     check_grad(tok, torch.randn(12000, 72, device=DEV), 200000, 1.0)
 
 
+@pytest.mark.parametrize("times", [7, 8, 9, 10])
+@pytest.mark.parametrize("T", [8191, 8192, 8193])
+def test_gradient_of_rows_named_equally_often(T, times):
+    """Rows on either side of the border between short and long ones, as many long
+    ones as fit, the last row of the table among them."""
+    V = (T + times - 1) // times
+    g = torch.Generator(device=DEV).manual_seed(T)
+    tok = (torch.arange(T, device=DEV) // times)[torch.randperm(T, generator=g, device=DEV)].int()
+    check_grad(tok, torch.randn(T, 36, generator=g, device=DEV).bfloat16(), V, 1.0)
+
+
 def test_gradient_ignores_tokens_outside():
     tok = torch.tensor([-1, 50, 2 ** 31 - 1, -2 ** 31, 3, 51, 49], dtype=torch.int32, device=DEV)
     check_grad(tok, torch.randn(7, 33, device=DEV), 50, 2.0)
