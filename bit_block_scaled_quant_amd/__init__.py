@@ -600,17 +600,47 @@ def gated_ffn_backward(dh, x: Quantized, x_t: Quantized, w: Quantized, act=SILU,
         raise ValueError(f"nvfp4: x_t must be the quantization of x^T, {K} x {M}, got {tuple(x_t.shape)}")
     if M % 16 or F % 8:
         raise ValueError(f"nvfp4: the backward needs M % 16 == 0 and F % 8 == 0, got M = {M}, F = {F}")
-    w_t = w.transposed()
-    dev = x.codes.device
-    q, qt = _alloc(M, 2 * F, dev, False), _alloc(2 * F, M, dev, False)
-    dgu = gated_ffn_grad(dh, x, w, act, amax=q.tensor_scale[1:])
-    if rht_t:  # the transformed copy has an amax of its own
-        nvfp4_quantize_cast_transpose(dgu, rounding, seed, seed_t, 1, rht_seed, q.codes, q.scales, q.tensor_scale,
-                                      qt.codes, qt.scales, qt.tensor_scale)
+    w_t, dev = w.transposed(), x.codes.device
+    # dgu and its two quantized copies share one allocation and go from call to
+    # call as addresses: what the calls would check of them holds by construction
+    if not isinstance(dh, torch.Tensor) or dh.dtype not in _IN:
+        _want(dh, "dh", _IN, dev)
+    args = (_arg(dh, "dh", _IN, dev, (M, F)), _dtype(dh),
+            *_ffn_args(x.codes, x.scales, x.tensor_scale, w.codes, w.scales, w.tensor_scale, M, F, K, dev))
+    w_args = (_arg(w_t.codes, "w's transposed codes", _U8, dev, (K, F)),
+              _arg(w_t.scales, "w's transposed scales", _U8, dev, (K, F // 8)),
+              _scale_arg(w_t.tensor_scale, "w_tensor_scale", dev))
+    x_args = (_arg(x_t.codes, "x_t's codes", _U8, dev, (K, M // 2)), _arg(x_t.scales, "x_t's scales", _U8, dev, (K, M // 16)),
+              _scale_arg(x_t.tensor_scale, "x_t's tensor_scale", dev))
+    dx = torch.empty(M, K, dtype=dtype, device=dev)
+    dw = torch.empty(2 * F, K, dtype=dtype, device=dev)
+    out, stream = _dtype(dx), _gpu_stream(dev)
+    size, at = 0, []
+    for n in (512, M * F, M * F, M * F // 8, M * F // 8, 2 * M * F * dh.element_size()):
+        at.append(size)
+        size += -(-n // 256) * 256
+    space = torch.empty(size, dtype=torch.uint8, device=dev)
+    base = space.data_ptr()
+    scale, codes, codes_t, scales, scales_t, dgu = (base + o for o in at)
+    scale_t = scale + 256
+    quantized = (codes, scales, scale, codes_t, scales_t, scale_t, stream)
+    L = lib()
+    rc = L.nvfp4_gated_ffn_grad(*args[2:], int(act), args[0], dgu, args[1], None if rht_t else scale + 4, stream)
+    if rc:
+        _check(rc, "nvfp4_gated_ffn_grad")
+    if rht_t:  # the transformed copy has an amax of its own, and the plain one's comes with it
+        rc = L.nvfp4_quantize_cast_transpose(dgu, args[1], M, 2 * F, int(rounding), int(seed), int(seed_t), 1,
+                                             int(rht_seed), *quantized)
     else:
-        nvfp4_quantize_cast_transpose_with_amax(dgu, rounding, seed, seed_t, q.codes, q.scales, q.tensor_scale,
-                                                qt.codes, qt.scales, qt.tensor_scale)
-    return gemm_ex(q, w_t, dtype=dtype), gemm_ex(qt, x_t, dtype=dtype)
+        rc = L.nvfp4_quantize_cast_transpose_with_amax(dgu, args[1], M, 2 * F, int(rounding), int(seed), int(seed_t),
+                                                       *quantized)
+    if rc:
+        _check(rc, "nvfp4_quantize_cast_transpose")
+    rc = (L.nvfp4_gemm_ex(codes, scales, scale, *w_args, M, K, 2 * F, dx.data_ptr(), out, 0.0, None, stream) or
+          L.nvfp4_gemm_ex(codes_t, scales_t, scale_t, *x_args, 2 * F, K, M, dw.data_ptr(), out, 0.0, None, stream))
+    if rc:
+        _check(rc, "nvfp4_gemm_ex")
+    return dx, dw
 
 
 # ---- distillation from a teacher's top logits ---------------------------------

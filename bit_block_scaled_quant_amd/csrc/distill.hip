@@ -280,8 +280,8 @@ __global__ __launch_bounds__(TH, TH == 1024 ? 4 : 1) void k_distill(DistillArgs 
     const int32_t at = s_idx[j];
     if (at < 0) continue;
     float target = 0.0f;  // an index named twice takes the sum, in the entries' order, from each of its threads
-    for (int i = 0; i < p.K; ++i)
-      if (s_idx[i] == at) target += s_p[i];
+#pragma unroll 8
+    for (int i = 0; i < p.K; ++i) target += s_idx[i] == at ? s_p[i] : 0.0f;
     dist_put<BF16>(g, at, (q(s_z[j]) - target * norm) * wt);
   }
 }
