@@ -389,7 +389,7 @@ __global__ __launch_bounds__(kGemmThreads, MT == 4 ? 1 : 2) void k_ffn_m32(FfnAr
 }
 
 // ---- few tokens: the weights are read once ----------------------------------
-// Up to 64 rows of X a workgroup.  A 16-row MFMA tile of W takes 8 gate rows
+// Up to 64 rows of X a workgroup (more go as row groups).  A 16-row MFMA tile of W takes 8 gate rows
 // and the up rows of the same 8 columns, so the chip's columns are dealt out in
 // eights: a workgroup owns TW tiles (8 TW columns) and all of K.  Its eight
 // waves take turns at the chunks of 128 H elements, straight from memory into
@@ -440,14 +440,14 @@ __global__ __launch_bounds__(kSkinnyThreads, 1) void k_ffn_skinny(FfnArgs p) {
   const GemmArgs& g = p.g;
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * (8 * TW);
+  const int64_t n0 = (int64_t)blockIdx.x * (8 * TW), m0 = (int64_t)blockIdx.y * (16 * MT);
   const uint32_t K = (uint32_t)g.K, kb = K / 2;
   const float ts_a = g.a_ts[0], ts_b = g.b_ts[0];
   uint32_t wr[TW], xr[MT];
 #pragma unroll
   for (int t = 0; t < TW; ++t) wr[t] = (uint32_t)(min(n0 + 8 * t + (li & 7), p.F - 1) + (li >> 3) * p.F);
 #pragma unroll
-  for (int i = 0; i < MT; ++i) xr[i] = (uint32_t)min<int64_t>(i * 16 + li, g.M - 1);
+  for (int i = 0; i < MT; ++i) xr[i] = (uint32_t)min<int64_t>(m0 + i * 16 + li, g.M - 1);
   floatx4 acc[MT][TW];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -529,7 +529,7 @@ __global__ __launch_bounds__(kSkinnyThreads, 1) void k_ffn_skinny(FfnArgs p) {
         u[k] += s_acc[s][v][from + 8][k0 + k];
       }
     }
-    const int64_t n = n0 + 8 * (v % TW) + (li & 7), m = 16 * (v / TW) + 4 * lg + k0;
+    const int64_t n = n0 + 8 * (v % TW) + (li & 7), m = m0 + 16 * (v / TW) + 4 * lg + k0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (m + k >= g.M || n >= p.F) continue;
@@ -545,36 +545,44 @@ __global__ __launch_bounds__(kSkinnyThreads, 1) void k_ffn_skinny(FfnArgs p) {
 
 static int64_t tiles_of(int64_t n, int64_t size) { return (n + size - 1) / size; }
 
-template <int MT, int TW, bool GRAD>
-static void launch_skinny_as(const FfnArgs& p, hipStream_t st) {
-  hipLaunchKernelGGL((k_ffn_skinny<MT, TW, GRAD>),
-                     dim3((unsigned)tiles_of(p.F, 8 * TW)), dim3(kSkinnyThreads), 0, st, p);
+// rows in groups of 16 MT <= 64, each with all columns, TW tiles of 8 a workgroup:
+// a CU's share, up to what the registers hold beside four row tiles
+struct SkinnyGrid {
+  int64_t cols, groups;
+  int mt, tw;
+};
+
+static SkinnyGrid skinny_grid(int64_t M, int64_t F, int cus) {
+  const int64_t rows = tiles_of(M, 16), groups = tiles_of(rows, 4), tiles = tiles_of(F, 8);
+  const int tw = (int)std::min<int64_t>(tiles_of(tiles * groups, cus), 5);
+  return {tiles_of(tiles, tw), groups, (int)tiles_of(rows, groups), tw};
 }
 
-// tiles of 8 columns for each CU, up to what the registers hold beside four row
-// tiles; wider blocks take more rounds
+template <int MT, int TW, bool GRAD>
+static void launch_skinny_as(const FfnArgs& p, const SkinnyGrid& gr, hipStream_t st) {
+  hipLaunchKernelGGL((k_ffn_skinny<MT, TW, GRAD>), dim3((unsigned)gr.cols, (unsigned)gr.groups), dim3(kSkinnyThreads),
+                     0, st, p);
+}
+
 template <int MT, bool GRAD>
-static void launch_skinny_mt(const FfnArgs& p, int cus, hipStream_t st) {
-  const int64_t each = tiles_of(tiles_of(p.F, 8), cus);
-  if (each <= 1)
-    launch_skinny_as<MT, 1, GRAD>(p, st);
-  else if (each <= 2)
-    launch_skinny_as<MT, 2, GRAD>(p, st);
-  else if (each <= 3)
-    launch_skinny_as<MT, 3, GRAD>(p, st);
-  else if (each == 4)
-    launch_skinny_as<MT, 4, GRAD>(p, st);
-  else
-    launch_skinny_as<MT, 5, GRAD>(p, st);
+static void launch_skinny_mt(const FfnArgs& p, const SkinnyGrid& gr, hipStream_t st) {
+  switch (gr.tw) {
+    case 1: return launch_skinny_as<MT, 1, GRAD>(p, gr, st);
+    case 2: return launch_skinny_as<MT, 2, GRAD>(p, gr, st);
+    case 3: return launch_skinny_as<MT, 3, GRAD>(p, gr, st);
+    case 4: return launch_skinny_as<MT, 4, GRAD>(p, gr, st);
+    default: return launch_skinny_as<MT, 5, GRAD>(p, gr, st);
+  }
 }
 
 template <bool GRAD>
 static void launch_skinny(const FfnArgs& p, int cus, hipStream_t st) {
-  switch (tiles_of(p.g.M, 16)) {
-    case 1: return launch_skinny_mt<1, GRAD>(p, cus, st);
-    case 2: return launch_skinny_mt<2, GRAD>(p, cus, st);
-    case 3: return launch_skinny_mt<3, GRAD>(p, cus, st);
-    default: return launch_skinny_mt<4, GRAD>(p, cus, st);
+  const SkinnyGrid gr = skinny_grid(p.g.M, p.F, cus);
+  switch (gr.mt) {
+    case 1: return launch_skinny_mt<1, GRAD>(p, gr, st);
+    case 2: return launch_skinny_mt<2, GRAD>(p, gr, st);
+    case 3: return launch_skinny_mt<3, GRAD>(p, gr, st);
+    default: return launch_skinny_mt<4, GRAD>(p, gr, st);
   }
 }
 
@@ -607,9 +615,14 @@ static void launch_m32_all(const FfnArgs& p, bool whole_k, hipStream_t st) {
 // whole rounds of the CUs as 256 x 128 tiles, what is left as 128 x 64 in a
 // second launch (M = 1024, F = 10240, K = 5120: 190 us; 240 in whole tiles, 202
 // in small ones).
-enum Tiles { kTile64x64, kTile128x64, kTile256x64, kTile256x128, kTileMixed };
+// Few columns leave most CUs without a tile; the kernel for few tokens then deals
+// out row groups too, at about 0.083 MT + 0.2 TW us for 256 K-elements and 0.1
+// MT TW (gradient 0.2) for the epilogue (128 rows of F = 2736, K = 2112: 19.8 us
+// in 64 x 64 tiles, 10.5 so; 256 rows of F = 256, K = 5120: 33 and 13.5; 1024 of
+// F = 512, K = 4096: 28 and 19).
+enum Tiles { kTile64x64, kTile128x64, kTile256x64, kTile256x128, kTileMixed, kTileSkinny };
 
-static Tiles choose_tiles(int64_t M, int64_t F, int64_t K, bool grad, int cus) {
+static Tiles choose_tiles(int64_t M, int64_t F, int64_t K, bool grad, bool skinny, int cus) {
   static const struct { int bm, bn; float fixed[2], stage[2]; } kCost[4] = {{64, 64, {0.75f, 2.2f}, {1.5f, 1.5f}},
                                                                            {128, 64, {2.0f, 5.0f}, {2.0f, 2.0f}},
                                                                            {256, 64, {5.6f, 13.0f}, {3.7f, 3.5f}},
@@ -628,6 +641,12 @@ static Tiles choose_tiles(int64_t M, int64_t F, int64_t K, bool grad, int cus) {
   const int64_t all = tiles_of(M, 256) * tiles_of(F, 128), left = all % cus;
   constexpr float kSecondLaunch = 4.0f;
   if (all > cus && left && rounds(3, all - left) + rounds(1, 4 * left) + kSecondLaunch < least) best = kTileMixed;
+  if (skinny) {
+    const SkinnyGrid gr = skinny_grid(M, F, cus);
+    const float fixed = 0.5f + (grad ? 0.2f : 0.1f) * gr.mt * gr.tw;
+    const float us = (float)tiles_of(gr.cols * gr.groups, cus) * (fixed + stages * (0.083f * gr.mt + 0.2f * gr.tw));
+    if (M <= 64 || us < least) best = kTileSkinny;
+  }
   return (Tiles)best;
 }
 
@@ -639,14 +658,13 @@ static void launch_ffn_t(const FfnArgs& p, int cus, hipStream_t st) {
   const bool stages = g.K % 64 == 0 && g.K <= (INT64_C(1) << 24) && (uintptr_t)g.a_codes % 16 == 0 &&
                       (uintptr_t)g.b_codes % 16 == 0 && (uintptr_t)g.a_scales % 4 == 0 &&
                       (uintptr_t)g.b_scales % 4 == 0;
-  if (stages && g.M <= 64 && p.F * g.K < (INT64_C(1) << 32)) {  // (its byte offsets are 32 bits)
-    launch_skinny<GRAD>(p, cus, st);
-    return;
-  }
   if (stages) {
     const bool whole_k =
         g.K % (2 * kDirBK) == 0 && (uintptr_t)g.a_scales % 16 == 0 && (uintptr_t)g.b_scales % 16 == 0;
-    switch (choose_tiles(g.M, p.F, g.K, GRAD, cus)) {
+    // the kernel for few tokens: byte offsets of 32 bits (and few row groups)
+    const bool skinny = g.M <= 2048 && g.M * g.K < (INT64_C(1) << 32) && p.F * g.K < (INT64_C(1) << 32);
+    switch (choose_tiles(g.M, p.F, g.K, GRAD, skinny, cus)) {
+      case kTileSkinny: launch_skinny<GRAD>(p, cus, st); break;
       case kTile64x64: launch_m32_all<2, 1, GRAD>(p, whole_k, st); break;
       case kTile128x64: launch_m32_all<2, 2, GRAD>(p, whole_k, st); break;
       case kTile256x64: launch_m32_all<2, 4, GRAD>(p, whole_k, st); break;

@@ -112,6 +112,14 @@ def test_few_tokens_column_shares(M, F, K, dtype):
     run(M, F, K, nv.GELU, dtype, seed=M + F)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M", [65, 81, 128, 143, 250, 513])
+@pytest.mark.parametrize("F,K", [(16, 5120), (250, 2112), (500, 4096), (1001, 1088), (2740, 2112)])
+def test_few_columns(M, F, K, dtype):
+    """Tall products with few columns and a long K, rows and columns ending inside a tile."""
+    run(M, F, K, nv.SILU, dtype, seed=M + F)
+
+
 @pytest.mark.parametrize("act", [nv.SILU, nv.GELU])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("M,F,K", [(2100, 2736, 832), (4096, 2048, 1024), (4000, 2100, 704), (3900, 2303, 512),
