@@ -6,7 +6,7 @@ The functions named like the C entry points (``nvfp4_quantize``,
 ``nvfp4_dequantize``, ``nvfp4_gemm``, ``nvfp4_gemm_ex``,
 ``nvfp4_quantize_with_amax``, and ``mxfp4_quantize``,
 ``mxfp4_dequantize``, ``mxfp4_gemm``, ``nvfp4_gated_ffn``,
-``nvfp4_gated_ffn_grad``, ``nvfp4_quantize_cast_transpose_with_amax``,
+``nvfp4_gated_ffn_grad``, ``nvfp4_quantize_cast_transpose_with_amax``, ``nvfp4_gemm_split``,
 ``nvfp4_distill_topk``, ``nvfp4_embed``, ``nvfp4_embed_grad``) only marshal torch
 tensors into pointers and the current HIP stream; every step of the
 computation runs in the library's HIP kernels.  There is no CPU fallback: if
@@ -15,7 +15,7 @@ the library is missing, or a tensor is not on the GPU, the call raises.
 Convenience wrappers (``quantize``, ``quantize_2d``,
 ``quantize_cast_transpose``, ``rht``, ``dequantize``, ``gemm``, ``mx_quantize``,
 ``mx_dequantize``, ``mx_gemm``, ``gated_ffn``, ``gated_ffn_grad``,
-``gated_ffn_backward``, ``distill_topk``, ``distill_topk_loss_and_grad``,
+``gated_ffn_backward``, ``gemm_split``, ``distill_topk``, ``distill_topk_loss_and_grad``,
 ``distill_topk_grad``, ``embed``, ``embed_grad``)
 allocate the outputs with torch (device memory only) and call the same
 entry points.
@@ -87,6 +87,8 @@ def lib():
         L.nvfp4_gated_ffn.argtypes = [P, P, P, P, P, P, I64, I64, I64, I, P, I, P]
         L.nvfp4_gated_ffn_grad.restype = I
         L.nvfp4_gated_ffn_grad.argtypes = [P, P, P, P, P, P, I64, I64, I64, I, P, P, I, P, P]
+        L.nvfp4_gemm_split.restype = I
+        L.nvfp4_gemm_split.argtypes = [P, P, P, P, P, P, I64, I64, I64, P, I, P]
         L.nvfp4_distill_topk.restype = I
         L.nvfp4_distill_topk.argtypes = [P, I, I64, I64, I64, P, P, I64, P, F, P, P, P, P]
         L.nvfp4_embed.restype = I
@@ -358,6 +360,18 @@ def nvfp4_gated_ffn_grad(x_codes, x_scales, x_tensor_scale, w_codes, w_scales, w
     rc = lib().nvfp4_gated_ffn_grad(*args, int(act), grad, out, _dtype(dgu), amax, _gpu_stream(dev))
     if rc:
         _check(rc, "nvfp4_gated_ffn_grad")
+
+
+def nvfp4_gemm_split(a_codes, a_scales, a_tensor_scale, b_codes, b_scales, b_tensor_scale, M, N, K, c):
+    dev = _out_device(c, "c")
+    out = _arg(c, "c", _IN, dev, (M, N))
+    rc = lib().nvfp4_gemm_split(
+        _arg(a_codes, "a_codes", _U8, dev, (M, K // 2)), _arg(a_scales, "a_scales", _U8, dev, (M, K // 16)),
+        _scale_arg(a_tensor_scale, "a_tensor_scale", dev), _arg(b_codes, "b_codes", _U8, dev, (N, K // 2)),
+        _arg(b_scales, "b_scales", _U8, dev, (N, K // 16)), _scale_arg(b_tensor_scale, "b_tensor_scale", dev),
+        M, N, K, out, _dtype(c), _gpu_stream(dev))
+    if rc:
+        _check(rc, "nvfp4_gemm_split")
 
 
 _I32 = (torch.int32,)
@@ -636,11 +650,21 @@ def gated_ffn_backward(dh, x: Quantized, x_t: Quantized, w: Quantized, act=SILU,
                                                        *quantized)
     if rc:
         _check(rc, "nvfp4_quantize_cast_transpose")
-    rc = (L.nvfp4_gemm_ex(codes, scales, scale, *w_args, M, K, 2 * F, dx.data_ptr(), out, 0.0, None, stream) or
-          L.nvfp4_gemm_ex(codes_t, scales_t, scale_t, *x_args, 2 * F, K, M, dw.data_ptr(), out, 0.0, None, stream))
+    rc = (L.nvfp4_gemm_split(codes, scales, scale, *w_args, M, K, 2 * F, dx.data_ptr(), out, stream) or
+          L.nvfp4_gemm_split(codes_t, scales_t, scale_t, *x_args, 2 * F, K, M, dw.data_ptr(), out, stream))
     if rc:
-        _check(rc, "nvfp4_gemm_ex")
+        _check(rc, "nvfp4_gemm_split")
     return dx, dw
+
+
+def gemm_split(a: Quantized, b: Quantized, out=None, dtype=torch.float32):
+    """deq(a) . deq(b)^T for products with few tiles and a long K (nvfp4_gemm_split)."""
+    (M, K), (N, K2) = a.shape, b.shape
+    if K != K2:
+        raise ValueError(f"K mismatch: {K} vs {K2}")
+    c = out if out is not None else torch.empty(M, N, dtype=dtype, device=a.codes.device)
+    nvfp4_gemm_split(a.codes, a.scales, a.tensor_scale, b.codes, b.scales, b.tensor_scale, M, N, K, c)
+    return c
 
 
 # ---- distillation from a teacher's top logits ---------------------------------

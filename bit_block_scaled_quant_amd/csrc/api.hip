@@ -320,6 +320,28 @@ int nvfp4_gated_ffn_grad(const uint8_t* x_codes, const uint8_t* x_scales, const 
                    dgu, dgu_amax, stream, "nvfp4_gated_ffn_grad");
 }
 
+int nvfp4_gemm_split(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_tensor_scale,
+                     const uint8_t* b_codes, const uint8_t* b_scales, const float* b_tensor_scale, int64_t M,
+                     int64_t N, int64_t K, void* c, int c_dtype, void* stream) {
+  if (!a_codes || !a_scales || !a_tensor_scale || !b_codes || !b_scales || !b_tensor_scale || !c)
+    return NVFP4_ERR_ARG;
+  if (c_dtype != NVFP4_F32 && c_dtype != NVFP4_BF16) return NVFP4_ERR_ARG;
+  if (M <= 0 || N <= 0 || K <= 0 || K % 16 != 0) return NVFP4_ERR_SHAPE;
+  if (!size_ok(M, K) || !size_ok(N, K) || !size_ok(M, N)) return NVFP4_ERR_SHAPE;
+  if (M > INT64_C(65535) * 128) return NVFP4_ERR_SHAPE;  // grid.y limit
+  if (!aligned(a_codes, 8) || !aligned(b_codes, 8) || !aligned(c, c_dtype == NVFP4_F32 ? 4 : 2) ||
+      !aligned(a_tensor_scale, 4) || !aligned(b_tensor_scale, 4))
+    return NVFP4_ERR_ALIGN;
+  int cus = 0;
+  int st = device_cus(&cus);
+  if (st) return st;
+  const bool f32 = c_dtype == NVFP4_F32;
+  nvfp4::GemmArgs g{a_codes, a_scales, a_tensor_scale, b_codes, b_scales, b_tensor_scale, M, N, K,
+                    f32 ? static_cast<float*>(c) : nullptr, f32 ? nullptr : static_cast<uint16_t*>(c), 0.0f, nullptr};
+  nvfp4::launch_gemm_split(g, cus, (hipStream_t)stream);
+  return check_launch("nvfp4_gemm_split");
+}
+
 int nvfp4_distill_topk(const void* logits, int dtype, int64_t T, int64_t V, int64_t stride, const int32_t* idx,
                        const float* top, int64_t K, const float* weight, float temperature, float* loss, float* lse,
                        void* grad, void* stream) {

@@ -429,23 +429,33 @@ __device__ __forceinline__ void skinny_load(const uint8_t* codes, const uint8_t*
   }
 }
 
-template <int MT, int TW, bool GRAD>
+// What it computes: the block, its gradient, or the plain product of X and F rows
+// of W, whose tiles are 16 columns each.
+enum SkinnyMode { kBlock, kBlockGrad, kProduct };
+
+// HALVES: K is only a multiple of 32, so rows start at any 16 bytes of codes and
+// two of scales.
+template <int MT, int TW, SkinnyMode MODE, bool HALVES = false>
 __global__ __launch_bounds__(kSkinnyThreads, 1) void k_ffn_skinny(FfnArgs p) {
+  constexpr bool GRAD = MODE == kBlockGrad;
+  constexpr int kCols = MODE == kProduct ? 16 : 8;  // columns of a tile
   // what a lane's 256 registers hold beside the sums: three whole lines of every
   // row, two, or halves of lines
   constexpr int kRows = MT + TW, kSums = 4 * MT * TW;
-  constexpr int H = 18 * kRows + kSums <= 210 ? 2 : 1;
+  constexpr int H = !HALVES && 18 * kRows + kSums <= 210 ? 2 : 1;
   constexpr int BUFS = (H == 2 ? 27 : 15) * kRows + kSums <= 200 ? 3 : 2;
   __shared__ __align__(16) float s_acc[kSkinnyWaves / 2][MT * TW][64][4];
   const GemmArgs& g = p.g;
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * (8 * TW), m0 = (int64_t)blockIdx.y * (16 * MT);
+  const int64_t n0 = (int64_t)blockIdx.x * (kCols * TW), m0 = (int64_t)blockIdx.y * (16 * MT);
   const uint32_t K = (uint32_t)g.K, kb = K / 2;
   const float ts_a = g.a_ts[0], ts_b = g.b_ts[0];
   uint32_t wr[TW], xr[MT];
 #pragma unroll
-  for (int t = 0; t < TW; ++t) wr[t] = (uint32_t)(min(n0 + 8 * t + (li & 7), p.F - 1) + (li >> 3) * p.F);
+  for (int t = 0; t < TW; ++t)
+    wr[t] = MODE == kProduct ? (uint32_t)min(n0 + 16 * t + li, p.F - 1)
+                             : (uint32_t)(min(n0 + 8 * t + (li & 7), p.F - 1) + (li >> 3) * p.F);
 #pragma unroll
   for (int i = 0; i < MT; ++i) xr[i] = (uint32_t)min<int64_t>(m0 + i * 16 + li, g.M - 1);
   floatx4 acc[MT][TW];
@@ -514,6 +524,23 @@ __global__ __launch_bounds__(kSkinnyThreads, 1) void k_ffn_skinny(FfnArgs p) {
   }
   __syncthreads();
 
+  if (MODE == kProduct) {  // lane (li, lg) holds rows 4 lg .. 4 lg + 3 of column li
+    const float inv_a = __fdiv_rn(1.0f, ts_a), inv_b = __fdiv_rn(1.0f, ts_b);
+    for (int v = wave; v < MT * TW; v += kSkinnyWaves) {
+      floatx4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < kHalf; ++s) {
+        const floatx4 d = *reinterpret_cast<const floatx4*>(s_acc[s][v][lane]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] += d[k];
+      }
+      const int64_t n = n0 + 16 * (v % TW) + li, m = m0 + 16 * (v / TW) + 4 * lg;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (m + k < g.M && n < p.F) put(p, (m + k) * p.F + n, (c[k] * inv_a) * inv_b);
+    }
+    return;
+  }
   // A tile's lane (li, lg) holds rows 4 lg .. 4 lg + 3 of gate column li (li <
   // 8) or up column li - 8; the lanes of such a pair emit two rows each.
   const float inv_a = __fdiv_rn(1.0f, ts_a), inv_b = __fdiv_rn(1.0f, ts_b);
@@ -560,7 +587,7 @@ static SkinnyGrid skinny_grid(int64_t M, int64_t F, int cus) {
 
 template <int MT, int TW, bool GRAD>
 static void launch_skinny_as(const FfnArgs& p, const SkinnyGrid& gr, hipStream_t st) {
-  hipLaunchKernelGGL((k_ffn_skinny<MT, TW, GRAD>), dim3((unsigned)gr.cols, (unsigned)gr.groups), dim3(kSkinnyThreads),
+  hipLaunchKernelGGL((k_ffn_skinny<MT, TW, GRAD ? kBlockGrad : kBlock>), dim3((unsigned)gr.cols, (unsigned)gr.groups), dim3(kSkinnyThreads),
                      0, st, p);
 }
 
@@ -692,6 +719,62 @@ void launch_ffn(const FfnArgs& p, int cus, hipStream_t st) {
     launch_ffn_t<true>(p, cus, st);
   else
     launch_ffn_t<false>(p, cus, st);
+}
+
+// ---- plain products with a long K and few tiles -----------------------------
+// The block's input and weight gradients contract over 2F or M; where the GEMM's
+// tiles leave most CUs idle, the kernel for few tokens takes the product
+// (M = 144, N = 576, K = 9216: 114 us in the GEMM's tiles, 18 so; [1000][1000] of
+// K = 4000: 92 and 18; 512 cubed: 14 and 8).
+template <int MT, int TW, bool HALVES>
+static void launch_product_as(const FfnArgs& p, int64_t groups, hipStream_t st) {
+  hipLaunchKernelGGL((k_ffn_skinny<MT, TW, kProduct, HALVES>),
+                     dim3((unsigned)tiles_of(p.F, 16 * TW), (unsigned)groups), dim3(kSkinnyThreads), 0, st, p);
+}
+
+template <int MT, bool HALVES>
+static void launch_product_mt(const FfnArgs& p, int64_t groups, int tw, hipStream_t st) {
+  if (tw == 1)
+    launch_product_as<MT, 1, HALVES>(p, groups, st);
+  else if (tw == 2)
+    launch_product_as<MT, 2, HALVES>(p, groups, st);
+  else
+    launch_product_as<MT, 4, HALVES>(p, groups, st);
+}
+
+template <bool HALVES>
+static void launch_product(const FfnArgs& p, int64_t groups, int mt, int tw, hipStream_t st) {
+  switch (mt) {
+    case 1: return launch_product_mt<1, HALVES>(p, groups, tw, st);
+    case 2: return launch_product_mt<2, HALVES>(p, groups, tw, st);
+    case 3: return launch_product_mt<3, HALVES>(p, groups, tw, st);
+    default: return launch_product_mt<4, HALVES>(p, groups, tw, st);
+  }
+}
+
+void launch_gemm_split(const GemmArgs& g, int cus, hipStream_t st) {
+  const bool fits = g.K % 32 == 0 && g.M <= INT64_C(65535) * 16 && g.M * g.K < (INT64_C(1) << 32) &&
+                    g.N * g.K < (INT64_C(1) << 32) && (uintptr_t)g.a_codes % 16 == 0 &&
+                    (uintptr_t)g.b_codes % 16 == 0 && (uintptr_t)g.a_scales % 4 == 0 && (uintptr_t)g.b_scales % 4 == 0;
+  const int64_t rows = tiles_of(g.M, 16), groups = tiles_of(rows, 4), cols = tiles_of(g.N, 16);
+  const int mt = (int)tiles_of(rows, groups), share = (int)std::min<int64_t>(tiles_of(cols * groups, cus), 4);
+  const int tw = share == 3 ? 4 : share;
+  const float stages = (float)tiles_of(g.K, 256);
+  const float split = (float)tiles_of(tiles_of(cols, tw) * groups, cus) *
+                      (0.5f + 0.1f * mt * tw + stages * (0.083f * mt + 0.2f * tw) * (g.K % 64 ? 1.25f : 1.0f));
+  // the GEMM: 128 x 128 tiles at 3.2 us for 256 K-elements, or whole 256 x 256 tiles at 6.1
+  const bool whole = g.M % 256 == 0 && g.N % 256 == 0 && g.K % 512 == 0;
+  const float gemm = whole ? (float)tiles_of(g.M / 256 * (g.N / 256), cus) * (10.0f + 6.1f * stages)
+                           : (float)tiles_of(tiles_of(g.M, 128) * tiles_of(g.N, 128), cus) * (4.0f + 3.2f * stages);
+  if (!fits || split >= gemm) {
+    launch_gemm(g, cus, st);
+    return;
+  }
+  FfnArgs p{g, g.N, 0, g.c16 != nullptr, nullptr, g.c16 ? (void*)g.c16 : (void*)g.c};
+  if (g.K % 64)
+    launch_product<true>(p, groups, mt, tw, st);
+  else
+    launch_product<false>(p, groups, mt, tw, st);
 }
 
 }  // namespace nvfp4

@@ -68,6 +68,8 @@ struct GemmArgs {
 };
 
 void launch_gemm(const GemmArgs& g, int cus, hipStream_t st);
+// the same product (beta 0, no amax), K divided among the waves of a workgroup where that is faster
+void launch_gemm_split(const GemmArgs& g, int cus, hipStream_t st);
 void launch_zero_amax(unsigned* p, hipStream_t st);  // *p = 0 (a kernel: captures into graphs)
 
 // Gated feed-forward block: [a | u] = deq(X) . deq(W)^T with W's first F rows

@@ -298,6 +298,18 @@ int nvfp4_gated_ffn_grad(const uint8_t* x_codes, const uint8_t* x_scales, const 
                          void* stream);
 
 /*
+ * C [M][N] = deq(A) . deq(B)^T as nvfp4_gemm_ex with beta = 0, for the block's
+ * two plain products: where the GEMM's tiles would leave most compute units
+ * idle, K is divided among the waves of a workgroup.  The sums are then taken
+ * in another fixed order, within the same tolerance, so the last bits may
+ * differ from nvfp4_gemm_ex's; results repeat bit for bit.
+ * Shapes, types and alignment as nvfp4_gemm_ex.
+ */
+int nvfp4_gemm_split(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_tensor_scale,
+                     const uint8_t* b_codes, const uint8_t* b_scales, const float* b_tensor_scale, int64_t M,
+                     int64_t N, int64_t K, void* c, int c_dtype, void* stream);
+
+/*
  * Distillation from a teacher's top logits.  For row r of logits (T rows of V,
  * `stride` >= V elements apart), z = logits / temperature and the entries
  * (idx [T][K], top [T][K]) of the teacher:

@@ -222,3 +222,21 @@ def test_cast_transpose_with_amax(dtype, rounding):
     for got, ref in zip((q, qt), want):
         assert torch.equal(got.codes, ref.codes) and torch.equal(got.scales, ref.scales)
         assert torch.equal(got.tensor_scale, ref.tensor_scale)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 32), (16, 16, 16), (17, 33, 96), (48, 100, 5120), (65, 130, 4128), (144, 576, 9216),
+                                   (500, 300, 2080), (130, 1000, 1024), (256, 256, 8192), (1000, 70, 3008),
+                                   (2050, 33, 1056), (70, 3000, 608), (300, 2500, 4160), (1024, 1024, 1024)])
+def test_split_product(M, N, K):
+    """nvfp4_gemm_split against the 64-bit product, within the GEMM's tolerance; bf16 is its rounding."""
+    g = torch.Generator(device=DEV).manual_seed(M + N)
+    a = nv.quantize(torch.randn(M, K, generator=g, device=DEV))
+    b = nv.quantize(torch.randn(N, K, generator=g, device=DEV) * 0.05)
+    va, vb = values(a), values(b)
+    buf = torch.full((M * N + 512,), 3.5, device=DEV)
+    c = nv.gemm_split(a, b, out=buf[256:256 + M * N].view(M, N))
+    bound = (K / 16 + 4) * 2.0 ** -24 * (va.abs() @ vb.abs().t().contiguous())
+    assert ((c.double() - va @ vb.t().contiguous()).abs() <= bound).all()
+    assert (buf[:256] == 3.5).all() and (buf[256 + M * N:] == 3.5).all()
+    assert torch.equal(c, nv.gemm_split(a, b))
+    assert torch.equal(nv.gemm_split(a, b, dtype=torch.bfloat16), c.bfloat16())

@@ -232,3 +232,19 @@ def test_embed_grad_workspace():
     assert size(0) == 0 and size(-1) == 0 and size(1 << 24) == 0
     assert size(1) >= 8192 * 8
     assert size(8193) >= 2 * 16384 * 8 + 8193 // 8 * 8
+
+
+def test_gemm_split_rejects():
+    a = dict(a_codes=z(32, 32), a_scales=z(32, 4), a_tensor_scale=z(2, dtype=F32), b_codes=z(48, 32), b_scales=z(48, 4),
+             b_tensor_scale=z(2, dtype=F32), M=32, N=48, K=64, c=z(32, 48, dtype=F32))
+    for name, bad in (("c", z(32, 47, dtype=F32)), ("c", z(32, 48)), ("a_codes", z(32, 31)), ("b_scales", z(47, 4)),
+                      ("a_tensor_scale", z(2)), ("b_codes", None)):
+        with pytest.raises((ValueError, TypeError), match=name):
+            nv.nvfp4_gemm_split(**{**a, name: bad})
+    with pytest.raises(ValueError, match="GPU memory"):
+        nv.nvfp4_gemm_split(**a)
+    call = nv.lib().nvfp4_gemm_split  # addresses are checked, never followed
+    ok = [256, 256, 256, 256, 256, 256, 32, 48, 64, 256, 0, None]
+    for at, value, status in ((0, None, -1), (9, None, -1), (10, 2, -1), (6, 0, -2), (7, -1, -2), (8, 24, -2), (8, 0, -2),
+                              (6, 65535 * 128 + 1, -2), (0, 260, -3), (2, 258, -3), (9, 258, -3)):
+        assert call(*[value if i == at else v for i, v in enumerate(ok)]) == status
